@@ -88,7 +88,8 @@ enum { PKV_QMODE_INT4_ASYM = 1, PKV_QMODE_FP8_E4M3 = 2 };
 enum {
     PKV_STATUS_BAD_BLOCK = 1,   /* block-table entry outside [0, num_blocks)     */
     PKV_STATUS_BAD_SLOT = 2,    /* slot outside [0, num_blocks * block_size)     */
-    PKV_STATUS_BAD_CONTEXT = 4, /* context_len < 0 or > max_blocks * block_size  */
+    PKV_STATUS_BAD_CONTEXT = 4, /* context_len < 0 or > max_blocks * block_size,
+                                 * or a sequence's row range out of order        */
     PKV_STATUS_BAD_PAIR = 8,    /* copy pair outside [0, num_blocks)             */
     PKV_STATUS_BAD_SINK = 16,   /* sink row / position outside its buffer        */
     PKV_STATUS_COPY_TIMEOUT = 32 /* a bounded wait for an asynchronous copy or a
@@ -156,6 +157,45 @@ int pkv_seq_append(pkv_pool* pool, int64_t seq, int32_t n_tokens, int64_t* slots
  * All-or-nothing across the whole batch. */
 int pkv_seq_append_batch(pkv_pool* pool, const int64_t* seqs, int32_t n, int32_t n_tokens_each,
                          int64_t* slots_out, int32_t* copy_pairs_out, int32_t* n_copies);
+
+/* Keep only the tokens at positions keep[0..n_keep) of seq (host int32,
+ * strictly ascending, in [0, length)), which become its positions 0, 1, ...
+ * in that order: eviction of tokens, or (keep = 0 .. n_keep - 1, which moves
+ * nothing) taking back the last ones, such as rejected draft tokens.
+ * Leading blocks whose rows all stay in place are kept as they are; the
+ * other kept rows go to fresh blocks, and the blocks they leave are given
+ * back (count - 1 each, in logical order).  Shared and cached blocks are
+ * never written.  With the first moved position f (the smallest i with
+ * keep[i] != i), the moves are the rows of positions block_size * (f /
+ * block_size) .. n_keep - 1:
+ *   src_slots_out, dst_slots_out  host int64[n_keep] (nullable when nothing
+ *                   moves): the slots to hand to pkv_move_rows, for every
+ *                   pool of every layer, before the new slots are read and
+ *                   before anything else is written to the blocks given
+ *                   back (stream order)
+ *   n_moves         host int32: their number
+ * No destination block is among the sources.  All-or-nothing: the fresh
+ * blocks are taken before any block is given back, and OUT_OF_BLOCKS leaves
+ * the pool and the sequence unchanged.  INVALID_ARG on a keep list that is
+ * not strictly ascending or leaves the sequence.  Sink rows and window rings
+ * of a quantised cache are kept by position, outside the pool: keep the sink
+ * positions (0 .. n_sink - 1) where they are.  A 16-bit window ring holds
+ * only the rows of the last window + block_size positions, so after a
+ * compaction it no longer matches: rewrite it (or attend with window 0). */
+int pkv_seq_compact(pkv_pool* pool, int64_t seq, const int32_t* keep, int32_t n_keep,
+                    int64_t* src_slots_out, int64_t* dst_slots_out, int32_t* n_moves);
+
+/* pkv_seq_compact for seqs[0..n-1] (distinct) at once: keep[keep_start[i] ..
+ * keep_start[i+1]) (host int32, keep_start [n + 1]) are sequence i's kept
+ * positions; the moves of all sequences, in that order, are one list (at most
+ * keep_start[n] - keep_start[0]) for one pkv_move_rows call.  Every fresh
+ * block is taken before any block is given back, so no destination block is
+ * any sequence's source; two pkv_seq_compact calls have no such guarantee
+ * towards each other, so launch the first one's moves before the second
+ * one's.  All-or-nothing across the batch. */
+int pkv_seq_compact_batch(pkv_pool* pool, const int64_t* seqs, int32_t n, const int32_t* keep,
+                          const int32_t* keep_start, int64_t* src_slots_out, int64_t* dst_slots_out,
+                          int32_t* n_moves);
 
 int pkv_seq_len(const pkv_pool* pool, int64_t seq, int64_t* out);
 int pkv_seq_num_blocks(const pkv_pool* pool, int64_t seq, int32_t* out);
@@ -397,6 +437,54 @@ int pkv_multi_query_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t 
                                     int32_t head_dim, int32_t max_blocks, int32_t block_size,
                                     int32_t max_q_len, size_t* out);
 
+/* Attention of whole prompts over K/V rows that are not (or not yet) in the
+ * cache: packed sequences, causal, grouped heads.  This is a prompt's own
+ * prefill, on the exact 16-bit rows the projections produced; pkv_kv_append
+ * or pkv_kv_append_quant stores the same rows for the decode steps that
+ * follow ("The 8GB VRAM Breakthrough", §5: the prefill computes the prompt's
+ * K/V once, before the decode loop).
+ *   q    [num_tokens, num_q_heads, head_dim], rows q_stride elements apart
+ *   k, v [num_kv_tokens, num_kv_heads, head_dim], rows k_stride / v_stride
+ *        elements apart (heads and dims contiguous): views of one fused
+ *        projection need no copy.  Strides are multiples of 8 elements (else
+ *        MISALIGNED) and at least one row long.
+ *   q_start, kv_start  device int32 [batch + 1], non-decreasing: sequence b
+ *        has the L_b = q_start[b+1] - q_start[b] query rows from q_start[b]
+ *        on and the S_b = kv_start[b+1] - kv_start[b] K/V rows from
+ *        kv_start[b] on.  kv_start may be NULL: the same rows as q_start.
+ *        The queries are the last L_b of the S_b positions:
+ *   out[q_start[b] + i, h] = sum_{t <= S_b - L_b + i} softmax_t(scale
+ *        <q, k_t>) v_t over KV head h / (num_q_heads / num_kv_heads); out is
+ *        [num_tokens, num_q_heads, head_dim], dense, in dtype.
+ * fp32 scores and sums; P enters the second product rounded to dtype.  Rows
+ * of no sequence (before q_start[0], from q_start[batch] on) are left as they
+ * were.  S_b < L_b, a start outside its rows or a decreasing one sets
+ * PKV_STATUS_BAD_CONTEXT (rows at negative positions get zeros; a bad range
+ * is cut to the rows there are).  A row does not depend on what later
+ * positions or other sequences hold, NaN and infinities included.  A row
+ * whose every score is -inf gets zeros.  scale: any finite value (else
+ * INVALID_ARG).
+ * workspace (device, nullable): with at least
+ * pkv_prompt_attention_workspace_bytes bytes, and that size non-zero, calls
+ * with few query rows over long K/V also split the K/V axis (fp32 partials
+ * merged by a second kernel); a workspace that is too small returns
+ * PKV_ERR_WORKSPACE.  Calls that share a workspace must not overlap on the
+ * GPU.  The waits of the kernel on its own copies and MMAs are bounded; one
+ * that runs out sets PKV_STATUS_COPY_TIMEOUT.
+ * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads <= 128. */
+int pkv_prompt_attention(const void* q, const void* k, const void* v, const int32_t* q_start,
+                         const int32_t* kv_start, int32_t batch, int32_t num_tokens,
+                         int32_t num_kv_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                         float scale, void* out, void* workspace, size_t workspace_bytes, int dtype,
+                         void* stream);
+
+/* Workspace bytes for pkv_prompt_attention's split: splits * num_tokens *
+ * num_q_heads * (head_dim + 2) * 4, 0 when the call is not split. */
+int pkv_prompt_attention_workspace_bytes(int32_t batch, int32_t num_tokens, int32_t num_kv_tokens,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, size_t* out);
+
 /* Allocation-free decode.  The source pages have no counterpart for this
  * entry point: it exists for callers that cannot provide a device workspace
  * -- code running while a stream is captured into a CUDA graph (allocation
@@ -490,6 +578,61 @@ int pkv_paged_attention_decode_quant(const void* q, const void* k_codes, const v
                                      int32_t group_size, float scale, void* out, void* workspace,
                                      size_t workspace_bytes, int32_t partition_size, int qmode,
                                      int dtype, void* stream);
+
+/* Multi-query attention over a quantised cache: the verify pass of
+ * speculative decoding over the pages' quantised cache ("The 8GB VRAM
+ * Breakthrough", §4 with §6), and slices of a chunked prefill (§5).
+ * Queries, positions and masks as pkv_paged_attention_multi_query (q_start,
+ * max_q_len; the L_b new tokens are the last L_b of context_lens[b], already
+ * appended); K_t, V_t as pkv_paged_attention_decode_quant reads them at
+ * context_lens[b]: dequantised codes, except positions t < n_sink (sink row
+ * b) and, with window > 0, the whole blocks from w0 = block_size *
+ * floor(max(context_lens[b] - window, 0) / block_size) on (window ring b).
+ * The same w0 holds for every query of the sequence.  L_b = 1 is
+ * pkv_paged_attention_decode_quant.  L_b > max_q_len sets
+ * PKV_STATUS_BAD_CONTEXT and computes the first max_q_len rows of the
+ * sequence only.  scale: any finite value (else INVALID_ARG).
+ * Two kernels, by the rows (query tokens x G) per (sequence, KV head):
+ *   - max_q_len * G <= 24: the balanced split over the (sequence, KV head,
+ *     block) items, each warp holding all rows of its runs, so each code is
+ *     read and unpacked once; a merge kernel follows.
+ *   - more rows: the 5th-generation tensor cores; blocks are dequantised once
+ *     per 256 rows into shared memory (as fp16: a dequantised value, and a
+ *     query, beyond +-65504 saturates there).
+ * workspace: device, at least pkv_multi_query_quant_workspace_bytes bytes
+ * (else WORKSPACE; may be NULL when that is 0).  Calls that share a
+ * workspace must not overlap on the GPU.
+ * Supported: as pkv_paged_attention_decode_quant (block_size 16, head_dim 64
+ * or 128, INT4 group_size == head_dim or 64, n_sink <= block_size, 1 <= G <=
+ * 8). */
+int pkv_paged_attention_multi_query_quant(
+    const void* q, const int32_t* q_start, const void* k_codes, const void* k_scale,
+    const void* k_zero, const void* v_codes, const void* v_scale, const void* v_zero,
+    const void* sink_k, const void* sink_v, int32_t n_sink, const void* win_k, const void* win_v,
+    int32_t window, const int32_t* block_tables, const int32_t* context_lens, int32_t batch,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+    int32_t block_size, int32_t max_blocks, int32_t max_q_len, int32_t group_size, float scale,
+    void* out, void* workspace, size_t workspace_bytes, int qmode, int dtype, void* stream);
+
+/* Workspace bytes for pkv_paged_attention_multi_query_quant. */
+int pkv_multi_query_quant_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t max_blocks, int32_t block_size,
+                                          int32_t max_q_len, size_t* out);
+
+/* Row moves (the device side of pkv_seq_compact): for every pool p, KV head h
+ * and move i, the row at dst_slots[i] becomes a byte copy of the row at
+ * src_slots[i], slot = block * block_size + offset.
+ *   pools          host array of n_pools device pointers (1..256), each
+ *                  [num_blocks, num_kv_heads, block_size, row]: K and V of
+ *                  every layer in one call; codes, scales and zeros too
+ *   bytes_per_row  host int64[n_pools], each > 0 and even
+ *   src_slots, dst_slots  device int64 [n_moves]
+ * A move with a negative slot is skipped; one with a slot beyond the pool
+ * sets PKV_STATUS_BAD_SLOT and is skipped.  No dst_slots entry may be another
+ * move's source or destination (pkv_seq_compact's never are). */
+int pkv_move_rows(void* const* pools, const int64_t* bytes_per_row, int32_t n_pools,
+                  const int64_t* src_slots, const int64_t* dst_slots, int32_t n_moves,
+                  int32_t num_blocks, int32_t num_kv_heads, int32_t block_size, void* stream);
 
 /* Copy-on-write block copy ("The 8GB VRAM Breakthrough", §3; "A Ideia de 60
  * Anos...", section "o bônus que paga o ingresso"): for each pair i,

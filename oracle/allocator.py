@@ -118,6 +118,42 @@ class KVCacheManager:
         del self.tables[sid]
         del self.lens[sid]
 
+    def compact(self, sids, keeps):
+        """Keep only the tokens at positions ``keeps[i]`` (ascending) of each
+        sequence ``sids[i]``.
+
+        Returns the moves of all sequences as ``(src_slots, dst_slots)``.
+        Leading blocks whose rows all stay in place are kept; every other kept
+        row gets a row of a fresh block.  All fresh blocks are taken before any
+        block is given back.
+        """
+        bs, plans = self.block_size, []
+        for sid, keep in zip(sids, keeps):
+            self._check(sid)
+            keep = [int(t) for t in keep]
+            if any(t < 0 or t >= self.lens[sid] for t in keep) or any(b <= a for a, b in zip(keep, keep[1:])):
+                raise ValueError("keep")
+            blocks = -(-len(keep) // bs)
+            start = 0
+            while start < blocks and keep[start * bs:(start + 1) * bs] == list(
+                    range(start * bs, min(len(keep), (start + 1) * bs))):
+                start += 1
+            plans.append((sid, keep, start, blocks))
+        if sum(blocks - start for _, _, start, blocks in plans) > self.pool.num_free():
+            raise OutOfBlocks()
+        src, dst, given_back = [], [], []
+        for sid, keep, start, blocks in plans:
+            old = self.tables[sid]
+            table = old[:start] + [self.pool.alloc() for _ in range(blocks - start)]
+            for i in range(start * bs, len(keep)):
+                src.append(old[keep[i] // bs] * bs + keep[i] % bs)
+                dst.append(table[i // bs] * bs + i % bs)
+            given_back += old[start:]
+            self.tables[sid], self.lens[sid] = table, len(keep)
+        for b in given_back:
+            self.pool.decref(b)
+        return src, dst
+
     def append(self, sid, n_tokens):
         """Reserve slots for ``n_tokens`` new tokens of sequence ``sid``.
 

@@ -162,3 +162,33 @@ def paged_multi_query_attention(q, q_start, k_pool, v_pool, block_tables, contex
             if ctx else np.zeros((0, Hkv, D))
         out[lo:hi] = multi_query_attention(q[lo:hi], k, v, scale)
     return out
+
+
+def prompt_attention(q, k, v, q_start, scale, kv_start=None):
+    """Causal attention of packed prompts over their own rows: sequence b's
+    queries (rows q_start[b] .. q_start[b+1]-1 of q [T, Hq, D]) are the last
+    of its K/V rows kv_start[b] .. kv_start[b+1]-1.  Returns float64
+    [T, Hq, D] and the same sum over |V| (the scale of a weighted sum's
+    rounding errors); rows of no sequence and rows at negative positions are
+    zero."""
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    kv_start = q_start if kv_start is None else kv_start
+    out, out_abs = np.zeros_like(q), np.zeros_like(q)
+    G = q.shape[1] // k.shape[1]
+    for b in range(len(q_start) - 1):
+        lo, hi = int(q_start[b]), int(q_start[b + 1])
+        ka, kb = int(kv_start[b]), int(kv_start[b + 1])
+        L, S = hi - lo, kb - ka
+        for i0 in range(0, L, 512):
+            pos = S - L + np.arange(i0, min(L, i0 + 512))
+            see = np.arange(S)[None] <= pos[:, None]
+            rows = slice(lo + i0, lo + i0 + len(pos))
+            for h in range(q.shape[1]):
+                x = (q[rows, h] @ k[ka:kb, h // G].T) * scale
+                x = np.where(see, x, -np.inf)
+                m = x.max(axis=1, keepdims=True, initial=-np.inf)
+                p = np.where(see, np.exp(x - np.where(np.isinf(m), 0.0, m)), 0.0)
+                p /= np.maximum(p.sum(axis=1, keepdims=True), 1e-300)
+                out[rows, h] = p @ v[ka:kb, h // G]
+                out_abs[rows, h] = p @ np.abs(v[ka:kb, h // G])
+    return out, out_abs

@@ -213,8 +213,33 @@ def sequence_attention_quant(q_seq, k_seq, v_seq, scale, n_sink, qmode, group_si
     return out
 
 
+def sequence_values(x_seq, n_sink, qmode, group_size, window=0):
+    """The float64 K or V values [ctx, Hkv, D] that attention reads for one
+    sequence of a quantised cache: dequantised codes, 16-bit sinks and window."""
+    if x_seq.shape[0] == 0:
+        return np.zeros(x_seq.shape)
+    deq = quantize_sequence(x_seq, qmode, group_size)[0]
+    ctx = x_seq.shape[0]
+    ns = min(n_sink, ctx)
+    deq[:ns] = np.asarray(x_seq[:ns], dtype=np.float64)
+    ws = window_start(ctx, window)
+    deq[ws:] = np.asarray(x_seq[ws:], dtype=np.float64)
+    return deq
+
+
 def copy_blocks(pools, pairs):
     """For each (src, dst): every pool's block dst becomes a copy of block src."""
     for src, dst in pairs:
         for p in pools:
             p[int(dst)] = p[int(src)]
+
+
+def move_rows(pools, src_slots, dst_slots, block_size=16):
+    """For each move: every pool's row (of every KV head) at slot dst becomes
+    a copy of the row at slot src.  pools: [num_blocks, Hkv, block_size, ...]."""
+    for src, dst in zip(src_slots, dst_slots):
+        src, dst = int(src), int(dst)
+        if src < 0 or dst < 0:
+            continue
+        for p in pools:
+            p[dst // block_size, :, dst % block_size] = p[src // block_size, :, src % block_size]

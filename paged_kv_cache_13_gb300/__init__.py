@@ -60,6 +60,8 @@ _SIGS = {
     "pkv_seq_fork": ([_vp, _i64, _p_i64], _int),
     "pkv_seq_append": ([_vp, _i64, _i32, _vp, _vp, _p_i32], _int),
     "pkv_seq_append_batch": ([_vp, _vp, _i32, _i32, _vp, _vp, _p_i32], _int),
+    "pkv_seq_compact": ([_vp, _i64, _vp, _i32, _vp, _vp, _p_i32], _int),
+    "pkv_seq_compact_batch": ([_vp, _vp, _i32, _vp, _vp, _vp, _vp, _p_i32], _int),
     "pkv_seq_len": ([_vp, _i64, _p_i64], _int),
     "pkv_seq_num_blocks": ([_vp, _i64, _p_i32], _int),
     "pkv_seq_block_table": ([_vp, _i64, _vp, _i32], _int),
@@ -79,6 +81,10 @@ _SIGS = {
          _vp, _sz, _int, _vp], _int),
     "pkv_multi_query_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)],
                                         _int),
+    "pkv_prompt_attention": (
+        [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _i64, _i64, _f32, _vp,
+         _vp, _sz, _int, _vp], _int),
+    "pkv_prompt_attention_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)], _int),
     "pkv_paged_attention_decode": (
         [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _sz,
          _i32, _int, _vp], _int),
@@ -99,6 +105,12 @@ _SIGS = {
     "pkv_paged_attention_decode_quant": (
         [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i32,
          _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _sz, _i32, _int, _int, _vp], _int),
+    "pkv_paged_attention_multi_query_quant": (
+        [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32,
+         _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _sz, _int, _int, _vp], _int),
+    "pkv_multi_query_quant_workspace_bytes": (
+        [_i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)], _int),
+    "pkv_move_rows": ([_vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp], _int),
     "pkv_copy_blocks": ([_vp, _vp, _i32, _vp, _i32, _i32, _vp], _int),
     "pkv_device_status": ([_p_i32, _vp], _int),
 }
@@ -252,6 +264,35 @@ def pkv_seq_append_batch(pool, seqs, n_tokens_each=1, slots_out=None, pairs_out=
     return slots_out[:n * n_tokens_each], pairs_out[:2 * nc.value].reshape(-1, 2)
 
 
+def pkv_seq_compact(pool, seq, keep):
+    """Keeps the tokens at positions keep (ascending) of seq; returns the
+    (src_slots, dst_slots) int64 arrays for pkv_move_rows (empty when no row
+    moves)."""
+    keep = np.ascontiguousarray(keep, dtype=np.int32)
+    n = keep.shape[0]
+    src, dst = (np.empty(max(n, 1), dtype=np.int64) for _ in range(2))
+    nm = _i32()
+    _check(lib.pkv_seq_compact(pool, seq, _ptr(keep), n, _ptr(src), _ptr(dst), ctypes.byref(nm)),
+           "pkv_seq_compact")
+    return src[:nm.value], dst[:nm.value]
+
+
+def pkv_seq_compact_batch(pool, seqs, keeps):
+    """pkv_seq_compact for several sequences (keeps: one position list each);
+    returns one (src_slots, dst_slots) pair for a single pkv_move_rows call."""
+    seqs = np.ascontiguousarray(seqs, dtype=np.int64)
+    if len(keeps) != seqs.shape[0]:
+        raise ValueError("one keep list per sequence")
+    start = np.concatenate([[0], np.cumsum([len(k) for k in keeps])]).astype(np.int32)
+    keep = np.concatenate([np.asarray(k, dtype=np.int32).reshape(-1) for k in keeps] or [np.empty(0, np.int32)])
+    keep = np.ascontiguousarray(keep, dtype=np.int32)
+    src, dst = (np.empty(max(int(start[-1]), 1), dtype=np.int64) for _ in range(2))
+    nm = _i32()
+    _check(lib.pkv_seq_compact_batch(pool, _ptr(seqs), seqs.shape[0], _ptr(keep), _ptr(start), _ptr(src), _ptr(dst),
+                                     ctypes.byref(nm)), "pkv_seq_compact_batch")
+    return src[:nm.value], dst[:nm.value]
+
+
 def pkv_seq_len(pool, seq):
     return _out_i64("pkv_seq_len", pool, seq)
 
@@ -385,6 +426,43 @@ def pkv_paged_attention_multi_query(q, q_start, k_pool, v_pool, block_tables, co
         _dtype_code(q), _stream(stream)), "pkv_paged_attention_multi_query")
 
 
+def _row_stride(t, name):
+    """Elements between the rows of t [T, H, D], whose rows are dense."""
+    T, H, D = t.shape
+    if T == 0:
+        return H * D
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError("%s: heads and dims must be contiguous within a row, got strides %s" % (name, t.stride()))
+    return t.stride(0) if T > 1 else max(t.stride(0), H * D)
+
+
+def pkv_prompt_attention_workspace_bytes(batch, num_tokens, num_kv_tokens, num_q_heads, num_kv_heads, head_dim):
+    v = _sz()
+    _check(lib.pkv_prompt_attention_workspace_bytes(batch, num_tokens, num_kv_tokens, num_q_heads, num_kv_heads,
+                                                    head_dim, ctypes.byref(v)),
+           "pkv_prompt_attention_workspace_bytes")
+    return v.value
+
+
+def pkv_prompt_attention(q, k, v, q_start, scale, out, kv_start=None, workspace=None, stream=None):
+    """Causal attention of packed prompts over their own K/V rows (no pages):
+    q [T, Hq, D], k, v [S, Hkv, D] (rows may be strided: views of one fused
+    projection), out [T, Hq, D] dense; q_start int32 [B + 1], kv_start the
+    same for k / v (None: q_start).  Sequence b's queries are the last of its
+    K/V positions."""
+    T, Hq, D = q.shape
+    S, Hkv, _ = k.shape
+    if v.shape != k.shape or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("v has k's shape; out is dense with q's shape")
+    if k.dtype != q.dtype or v.dtype != q.dtype or out.dtype != q.dtype:
+        raise TypeError("q, k, v and out have one dtype")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.pkv_prompt_attention(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(q_start), _ptr(kv_start), q_start.shape[0] - 1, T, S, Hq, Hkv, D,
+        _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v"), float(scale), _ptr(out), _ptr(workspace),
+        ws_bytes, _dtype_code(q), _stream(stream)), "pkv_prompt_attention")
+
+
 def pkv_paged_attention_decode_append(q, k_new, v_new, slot_mapping, k_pool, v_pool, block_tables,
                                       context_lens, scale, out, workspace=None, partition_size=0,
                                       stream=None):
@@ -469,6 +547,50 @@ def pkv_paged_attention_decode_quant(q, cache, n_sink, block_tables, context_len
         _ptr(context_lens), B, Hq, Hkv, D, NB, BS, block_tables.shape[1], group_size or D,
         float(scale), _ptr(out), _ptr(workspace), ws_bytes, partition_size, _qmode_code(qmode),
         _dtype_code(q), _stream(stream)), "pkv_paged_attention_decode_quant")
+
+
+def pkv_multi_query_quant_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_blocks, max_q_len,
+                                          block_size=16):
+    v = _sz()
+    _check(lib.pkv_multi_query_quant_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_blocks,
+                                                     block_size, int(max_q_len), ctypes.byref(v)),
+           "pkv_multi_query_quant_workspace_bytes")
+    return v.value
+
+
+def pkv_paged_attention_multi_query_quant(q, q_start, cache, n_sink, block_tables, context_lens, scale, out,
+                                          max_q_len, qmode, group_size=0, workspace=None, stream=None, window=0):
+    """q, out [T, Hq, D]; q_start int32 [B + 1]; cache as pkv_kv_append_quant
+    wrote it.  workspace: device bytes (pkv_multi_query_quant_workspace_bytes)."""
+    T, Hq, D = q.shape
+    kc = cache["k_codes"]
+    NB, Hkv, BS, _ = kc.shape
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.pkv_paged_attention_multi_query_quant(
+        _ptr(q), _ptr(q_start), _ptr(kc), _ptr(cache["k_scale"]), _ptr(cache.get("k_zero")),
+        _ptr(cache["v_codes"]), _ptr(cache["v_scale"]), _ptr(cache.get("v_zero")), _ptr(cache.get("sink_k")),
+        _ptr(cache.get("sink_v")), n_sink, _ptr(cache.get("win_k")), _ptr(cache.get("win_v")), window,
+        _ptr(block_tables), _ptr(context_lens), q_start.shape[0] - 1, Hq, Hkv, D, NB, BS, block_tables.shape[1],
+        int(max_q_len), group_size or D, float(scale), _ptr(out), _ptr(workspace), ws_bytes, _qmode_code(qmode),
+        _dtype_code(q), _stream(stream)), "pkv_paged_attention_multi_query_quant")
+
+
+def pkv_move_rows(pools, src_slots, dst_slots, stream=None):
+    """pools: list of device tensors [NB, Hkv, BS, ...] (K and V of every
+    layer, codes, scales, zeros); src_slots, dst_slots: device int64 [n]."""
+    n = src_slots.shape[0]
+    if dst_slots.shape[0] != n:
+        raise ValueError("src_slots and dst_slots have one length")
+    if n == 0:
+        return
+    NB, Hkv, BS = pools[0].shape[:3]
+    for p in pools:
+        if tuple(p.shape[:3]) != (NB, Hkv, BS) or not p.is_contiguous():
+            raise ValueError("pools are dense [num_blocks, num_kv_heads, block_size, ...] of one shape")
+    ptrs = (_vp * len(pools))(*[p.data_ptr() for p in pools])
+    bpr = (_i64 * len(pools))(*[p[0, 0, 0].numel() * p.element_size() for p in pools])
+    _check(lib.pkv_move_rows(ptrs, bpr, len(pools), _ptr(src_slots), _ptr(dst_slots), n, NB, Hkv, BS,
+                             _stream(stream)), "pkv_move_rows")
 
 
 def pkv_copy_blocks(pools, pairs, stream=None):

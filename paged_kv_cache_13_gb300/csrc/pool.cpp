@@ -341,6 +341,87 @@ int pkv_seq_append_batch(pkv_pool* pool, const int64_t* seqs, int32_t n, int32_t
     return PKV_OK;
 }
 
+int pkv_seq_compact_batch(pkv_pool* pool, const int64_t* seqs, int32_t n, const int32_t* keep,
+                          const int32_t* keep_start, int64_t* src_slots_out, int64_t* dst_slots_out,
+                          int32_t* n_moves) {
+    if (!pool) return PKV_ERR_BAD_HANDLE;
+    if (n < 0 || !n_moves || (n > 0 && (!seqs || !keep_start))) return PKV_ERR_INVALID_ARG;
+    struct Plan {
+        Seq* s;
+        const int32_t* keep;
+        int32_t n_keep, start, fresh, moves;
+    };
+    const int32_t bs = pool->block_size;
+    int64_t fresh = 0, moves = 0;
+    std::vector<Plan> plans;
+    std::vector<int32_t> left;  // the blocks given back
+    try {                       // every allocation before anything changes
+        plans.reserve(n);
+        size_t blocks_left = 0;
+        for (int32_t i = 0; i < n; ++i) {
+            auto it = pool->seqs.find(seqs[i]);
+            if (it == pool->seqs.end()) return PKV_ERR_BAD_SEQ;
+            Plan p;
+            p.s = &it->second;
+            for (const Plan& o : plans)
+                if (o.s == p.s) return PKV_ERR_INVALID_ARG;  // duplicates
+            if (keep_start[i] < 0 || keep_start[i + 1] < keep_start[i] || (keep_start[i + 1] > keep_start[i] && !keep))
+                return PKV_ERR_INVALID_ARG;
+            p.keep = keep ? keep + keep_start[i] : nullptr;
+            p.n_keep = keep_start[i + 1] - keep_start[i];
+            for (int32_t j = 0; j < p.n_keep; ++j)
+                if (p.keep[j] < 0 || p.keep[j] >= p.s->len || (j > 0 && p.keep[j] <= p.keep[j - 1]))
+                    return PKV_ERR_INVALID_ARG;
+            int32_t f = 0;  // the first position whose row moves
+            while (f < p.n_keep && p.keep[f] == f) ++f;
+            const int32_t blocks = static_cast<int32_t>((static_cast<int64_t>(p.n_keep) + bs - 1) / bs);
+            // blocks [0, start) stay; the kept rows behind them go to fresh blocks
+            p.start = f == p.n_keep ? blocks : f / bs;
+            p.fresh = blocks - p.start;
+            p.moves = p.fresh > 0 ? p.n_keep - p.start * bs : 0;
+            fresh += p.fresh;
+            moves += p.moves;
+            blocks_left += p.s->table.size() - p.start;
+            plans.push_back(p);
+        }
+        left.reserve(blocks_left);
+    } catch (const std::bad_alloc&) {
+        return PKV_ERR_INVALID_ARG;
+    }
+    if (moves > INT32_MAX || (moves > 0 && (!src_slots_out || !dst_slots_out))) return PKV_ERR_INVALID_ARG;
+    if (fresh > pool->allocatable()) return PKV_ERR_OUT_OF_BLOCKS;
+    int64_t m = 0;
+    for (Plan& p : plans) {
+        auto& table = p.s->table;
+        left.insert(left.end(), table.begin() + p.start, table.end());
+        for (int32_t i = 0; i < p.moves; ++i) {
+            const int32_t t = p.keep[p.start * bs + i];
+            src_slots_out[m + i] = static_cast<int64_t>(table[t / bs]) * bs + t % bs;
+        }
+        for (int32_t j = 0; j < p.fresh; ++j) table[p.start + j] = pool->alloc_unchecked();
+        table.resize(p.start + p.fresh);  // never grows: n_keep <= length
+        for (int32_t i = 0; i < p.moves; ++i)
+            dst_slots_out[m + i] = static_cast<int64_t>(table[p.start + i / bs]) * bs + i % bs;
+        m += p.moves;
+        p.s->len = p.n_keep;
+    }
+    // only now: no block given back is handed out again within this call, so
+    // no destination is another sequence's source
+    for (int32_t b : left) {
+        const int st = pool->decref(b);
+        if (st != PKV_OK) return st;  // only reachable if the state was corrupted
+    }
+    *n_moves = static_cast<int32_t>(m);
+    return PKV_OK;
+}
+
+int pkv_seq_compact(pkv_pool* pool, int64_t seq, const int32_t* keep, int32_t n_keep,
+                    int64_t* src_slots_out, int64_t* dst_slots_out, int32_t* n_moves) {
+    if (pool && n_keep < 0) return PKV_ERR_INVALID_ARG;
+    const int32_t keep_start[2] = {0, n_keep};
+    return pkv_seq_compact_batch(pool, &seq, 1, keep, keep_start, src_slots_out, dst_slots_out, n_moves);
+}
+
 int pkv_seq_len(const pkv_pool* pool, int64_t seq, int64_t* out) {
     if (!pool) return PKV_ERR_BAD_HANDLE;
     if (!out) return PKV_ERR_INVALID_ARG;
