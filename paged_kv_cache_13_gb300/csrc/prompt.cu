@@ -49,6 +49,7 @@ constexpr float kSlack = 8.f;  // log2 units a score may exceed the reference ma
 constexpr int kRows = 128;     // query rows per MMA tile
 constexpr int kCtaRows = 256;  // two tiles
 constexpr int kKeys = 128;     // keys per tile
+constexpr int kFirst = 64;     // keys of P handed to the MMAs before the rest is computed
 constexpr int kThreads = 384;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8: copies; 9: MMAs
 constexpr int kWarpLoad = 8, kWarpMma = 9;
 // Registers: launched at 168 a thread; the softmax warpgroups take 232, the
@@ -64,7 +65,7 @@ struct Layout {
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = 2 * kTile;
     static constexpr int kOffBar = kOffRing + kStages * kTile;
-    static constexpr int kFull = 0, kFree = kStages, kS = 2 * kStages, kP = kS + 2, kO = kP + 2, kDrain = kO + 2;
+    static constexpr int kFull = 0, kFree = kStages, kS = 2 * kStages, kP = kS + 2, kO = kP + 4, kDrain = kO + 2;
     static constexpr int kBars = kDrain + 1;
     static constexpr int kOffVars = kOffBar + 8 * kBars;
     static constexpr int kBytes = kOffVars + 16 + 1024;  // and the alignment of the base
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* stop_flag = reinterpret_cast<int*>(sm + Y::kOffVars + 4);
     volatile int* odd_flag = reinterpret_cast<int*>(sm + Y::kOffVars + 8);  // a non-finite V value was taken out
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // slots from the last one down: a sequence's later rows see more keys
     const int per_slot = a.hkv * a.splits;
     const int u = (gridDim.x - 1 - blockIdx.x) / per_slot;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = max(cnt[0], cnt[1]);
 
     if (tid == 0) {
-        for (int i = 0; i < Y::kBars; ++i) mbar_init(bar(i), i == Y::kP || i == Y::kP + 1 ? 4 : 1);
+        for (int i = 0; i < Y::kBars; ++i) mbar_init(bar(i), i >= Y::kP && i < Y::kP + 4 ? 4 : 1);
         *stop_flag = 0;
         *odd_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -262,35 +263,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             // shared memory is given up
             if (stopped())
                 for (int x = max(it - Y::kStages, 0); x < it; ++x) wait_bar(bar(Y::kFull + slot(x)), phase(x));
-        } else if (warp == kWarpMma && lane == 0 && n > 0) {
-            const uint32_t id_s = instr_desc<T>(kKeys, false), id_o = instr_desc<T>(D, true);
-            auto issue_s = [&](int i, int it) {
-                const uint32_t qa = sbase + Y::kOffQ + i * Y::kTile, kb = sbase + Y::kOffRing + slot(it) * Y::kTile;
+        } else if (warp == kWarpMma && n > 0) {
+            // The whole warp walks the loop, one elected lane issues: what the
+            // MMAs take is then warp-uniform (base descriptors plus constants),
+            // and an MMA of K 16 costs its 64 cycles; issued from a lane of a
+            // divergent branch it cost ~110 (8,192 tokens: 490 us).
+            constexpr uint32_t id_s = instr_desc<T>(kKeys, false), id_o = instr_desc<T>(D, true);
+            constexpr uint32_t kTile16 = Y::kTile >> 4;  // descriptor units
+            const bool el = elect();
+            const uint64_t dq = smem_desc(sbase + Y::kOffQ, 16384, 1024);
+            const uint64_t dr = smem_desc(sbase + Y::kOffRing, 16384, 1024);
+            auto issue_s = [&](int i, int s) {
+                const uint64_t qa = dq + i * kTile16, kb = dr + s * kTile16;
+                if (el) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
-                    mma_ss(tmem + i * kKeys, smem_desc(qa + off, 16384, 1024), smem_desc(kb + off, 16384, 1024), id_s,
-                           kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        constexpr uint32_t kHalf16 = (kRows * 128) >> 4;
+                        const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
+                        mma_ss(tmem + i * kKeys, qa + off, kb + off, id_s, kk > 0);
+                    }
+                    mma_commit(bar(Y::kS + i));
                 }
-                mma_commit(bar(Y::kS + i));
             };
-            auto issue_o = [&](int i, int it, bool acc) {
-                const uint32_t vb = sbase + Y::kOffRing + slot(it) * Y::kTile;
+            // keys 16 k0 .. 16 k1 - 1
+            auto issue_o = [&](int i, int s, int k0, int k1, bool acc) {
+                const uint64_t vb = dr + s * kTile16;
+                if (el) {
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_ts(tmem + 2 * kKeys + i * kKeys, tmem + i * kKeys + kk * 8,
-                           smem_desc(vb + kk * 2048, 16384, 1024), id_o, acc || kk > 0);
+                    for (int kk = k0; kk < k1; ++kk)
+                        mma_ts(tmem + 2 * kKeys + i * kKeys, tmem + i * kKeys + kk * 8, vb + kk * 128, id_o,
+                               acc || kk > 0);
+                }
             };
-            bool ok = wait_bar(bar(Y::kFull + slot(0)), phase(0));
+            auto next = [&](int& s, uint32_t& ph) {
+                if (++s == Y::kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            };
+            int s = 0;  // ring slot and its phase, walking K0 V0 K1 V1 ..
+            uint32_t ph = 0;
+            bool ok = wait_bar(bar(Y::kFull), 0);
             if (ok) {
                 fence_after_sync();
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (cnt[i] > 0) issue_s(i, 0);
-                mma_commit(bar(Y::kFree + slot(0)));
+                if (el) mma_commit(bar(Y::kFree));
             }
+            next(s, ph);
             for (int jj = 0; ok && jj < n; ++jj) {
-                ok = !stopped() && wait_bar(bar(Y::kFull + slot(2 * jj + 1)), phase(2 * jj + 1));
+                const int sv = s;  // V(jj), then K(jj + 1)
+                ok = !stopped() && wait_bar(bar(Y::kFull + sv), ph);
+                next(s, ph);
                 bool have_k = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -298,26 +323,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait_bar(bar(Y::kP + i), jj & 1);
                     if (!ok) continue;
                     fence_after_sync();
-                    issue_o(i, 2 * jj + 1, jj > 0);
+                    issue_o(i, sv, 0, kFirst / 16, jj > 0);
+                    ok = wait_bar(bar(Y::kP + 2 + i), jj & 1);
+                    if (!ok) continue;
+                    fence_after_sync();
+                    issue_o(i, sv, kFirst / 16, kKeys / 16, true);
                     if (jj + 1 < cnt[i]) {
-                        if (!have_k) ok = wait_bar(bar(Y::kFull + slot(2 * jj + 2)), phase(2 * jj + 2));
+                        if (!have_k) ok = wait_bar(bar(Y::kFull + s), ph);
                         have_k = ok;
                         if (ok) {
                             fence_after_sync();
-                            issue_s(i, 2 * jj + 2);
+                            issue_s(i, s);
                         }
-                    } else {
+                    } else if (el) {
                         mma_commit(bar(Y::kO + i));
                     }
                 }
                 if (!ok) break;
-                mma_commit(bar(Y::kFree + slot(2 * jj + 1)));
-                if (jj + 1 < n) mma_commit(bar(Y::kFree + slot(2 * jj + 2)));
+                if (el) {
+                    mma_commit(bar(Y::kFree + sv));
+                    if (jj + 1 < n) mma_commit(bar(Y::kFree + s));
+                }
+                next(s, ph);
             }
-            if (!ok) give_up();
+            if (!ok && lane == 0) give_up();
             // every MMA and every arrival of theirs is done (bounded) before
             // the CTA gives up its shared memory and TMEM
-            mma_commit(bar(Y::kDrain));
+            if (el) mma_commit(bar(Y::kDrain));
             wait_bar(bar(Y::kDrain), 0);
         }
     } else {
@@ -373,24 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = mx;
                 l *= alpha;
             }
-            const float mref = m == neg_inf() ? 0.f : m;
-            const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-mref, -mref);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float2 e = fma2(make_float2(x[hb * 64 + 2 * i], x[hb * 64 + 2 * i + 1]), mul2, ref2);
-                    e.x = ex2(e.x);
-                    e.y = ex2(e.y);
-                    sum[i & 1] = add2(sum[i & 1], e);
-                    p[i] = Half16<T>::pack(e.x, e.y);
-                }
-                tmem_st32(tS + hb * 32, p);
-            }
-            const float2 s2 = add2(sum[0], sum[1]);
-            l += s2.x + s2.y;
             if (jj > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
@@ -438,10 +452,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_async_shared();
                 }
             }
-            tmem_wait_st();
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(Y::kP + tile));
+            // P in steps of 32 keys; the first kFirst are handed over early
+            const float mref = m == neg_inf() ? 0.f : m;
+            const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-mref, -mref);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int cc = 0; cc < kKeys / 32; ++cc) {
+                uint32_t p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float2 e = fma2(make_float2(x[cc * 32 + 2 * i], x[cc * 32 + 2 * i + 1]), mul2, ref2);
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    sum[i & 1] = add2(sum[i & 1], e);
+                    p[i] = Half16<T>::pack(e.x, e.y);
+                }
+                tmem_st16(tS + cc * 16, p);
+                if (cc + 1 == kFirst / 32 || cc + 1 == kKeys / 32) {
+                    tmem_wait_st();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(Y::kP + (cc + 1 == kKeys / 32 ? 2 : 0) + tile));
+                }
+            }
+            const float2 s2 = add2(sum[0], sum[1]);
+            l += s2.x + s2.y;
         }
         if (ok && my_cnt > 0) {
             ok = wait_bar(bar(Y::kO + tile), 0);
