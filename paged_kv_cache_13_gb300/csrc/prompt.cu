@@ -101,6 +101,18 @@ __device__ __forceinline__ bool find_job(const int32_t* q_start, const int32_t* 
     const int lane = threadIdx.x & 31;
     auto start = [&](int b) { return min(max(q_start[b], 0), T); };
     int lo = 0, n = batch;
+    int qa, qe, ka, ke;
+    if (batch < 32) {  // every start in one round of loads
+        const int qv = lane <= batch ? start(lane) : 0, kv = lane <= batch ? min(max(kv_start[lane], 0), S) : 0;
+        const unsigned le = __ballot_sync(0xffffffffu, lane < batch &&
+                                                           static_cast<int64_t>(qv) * G / kCtaRows + lane <= u);
+        if (le == 0) return false;
+        lo = __popc(le) - 1;
+        qa = __shfl_sync(0xffffffffu, qv, lo);
+        qe = __shfl_sync(0xffffffffu, qv, lo + 1);
+        ka = __shfl_sync(0xffffffffu, kv, lo);
+        ke = __shfl_sync(0xffffffffu, kv, lo + 1);
+    } else {
     for (;;) {
         const int step = (n + 31) / 32;
         const int b = lo + lane * step;
@@ -112,11 +124,16 @@ __device__ __forceinline__ bool find_job(const int32_t* q_start, const int32_t* 
         n = min(step, n - (c - 1) * step);
         if (n == 1) break;
     }
+    qa = start(lo);
+    qe = start(lo + 1);
+    ka = min(max(kv_start[lo], 0), S);
+    ke = min(max(kv_start[lo + 1], 0), S);
+    }
     job.b = lo;
-    job.q0 = start(lo);
-    job.L = start(lo + 1) - job.q0;
-    job.k0 = min(max(kv_start[lo], 0), S);
-    job.S = max(min(max(kv_start[lo + 1], 0), S) - job.k0, 0);
+    job.q0 = qa;
+    job.L = qe - qa;
+    job.k0 = ka;
+    job.S = max(ke - ka, 0);
     if (job.L <= 0) return false;
     const int64_t off = static_cast<int64_t>(job.q0) * G / kCtaRows + lo;
     const int64_t row0 = (u - off) * kCtaRows;
@@ -202,36 +219,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) cnt[i] = max(min(cnt[i], je) - js, 0);
     const int n = max(cnt[0], cnt[1]);
 
-    if (tid == 0) {
+    // ring item 2 jj is K of the jj-th tile, 2 jj + 1 its V
+    auto slot = [&](int it) { return it % Y::kStages; };
+    auto phase = [&](int it) { return static_cast<uint32_t>(it / Y::kStages) & 1u; };
+    auto load_item = [&](int it) {
+        const int s = slot(it);
+        mbar_arrive_expect_tx(bar(Y::kFull + s), Y::kTile);
+        tma_load(sbase + Y::kOffRing + s * Y::kTile, it & 1 ? &vmap : &kmap, job.k0 + (js + it / 2) * kKeys, kvh,
+                 bar(Y::kFull + s));
+    };
+    const int early = min(2 * n, Y::kStages);  // items the empty ring takes
+    const int tile = warp >> 2;                // softmax: 0 or 1
+    if (warp == kWarpLoad && lane == 0) {
         for (int i = 0; i < Y::kBars; ++i) mbar_init(bar(i), i >= Y::kP && i < Y::kP + 4 ? 4 : 1);
         *stop_flag = 0;
         *odd_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncwarp();
-    if (warp == 0) {
+        fence_async_shared();
+        for (int it = 0; it < early; ++it) load_item(it);  // on their way while Q is fetched
+    } else if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sh_addr(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (tile < 2) {
+        // the warp's 32 query rows, whole 128-byte lines at a time: lane l
+        // takes chunk l % kCh of rows l / kCh, l / kCh + kStep, ..
+        constexpr int kStep = 32 / kCh;
+        const int rr0 = (warp & 3) * 32 + lane / kCh, ch = lane % kCh;
+        int row = job.row0 + tile * kRows + rr0;
+        int tok = row / a.G, h = row - tok * a.G;
+        const T* base = static_cast<const T*>(a.q) + static_cast<int64_t>(job.q0) * a.qs + kvh * a.G * D + ch * 8;
+        uint4 w[kCh];
+#pragma unroll
+        for (int x = 0; x < kCh; ++x) {
+            w[x] = make_uint4(0, 0, 0, 0);
+            if (row < job.rows) w[x] = *reinterpret_cast<const uint4*>(base + tok * a.qs + h * D);
+            row += kStep;
+            h += kStep;
+            while (h >= a.G) {
+                h -= a.G;
+                ++tok;
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kCh; ++x)
+            *reinterpret_cast<uint4*>(sm + Y::kOffQ + tile * Y::kTile + tile_off(rr0 + x * kStep, ch)) = w[x];
+        fence_async_shared();
     }
-    const int tile = warp >> 2;                // softmax: 0 or 1
-    const int r = (warp & 3) * 32 + lane;      // and its row there (also its TMEM lane)
+    const int r = (warp & 3) * 32 + lane;  // softmax: the thread's row of the tile (and TMEM lane)
     const int row = job.row0 + tile * kRows + r;
     const int tok = row / a.G, h = row - tok * a.G;
     const bool valid = row < job.rows;
-    if (tile < 2) {  // the thread's query row
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                          (static_cast<int64_t>(job.q0) + tok) * a.qs +
-                                                          (kvh * a.G + h) * D);
-        uint4 w[kCh];
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch) w[ch] = valid ? src[ch] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch)
-            *reinterpret_cast<uint4*>(sm + Y::kOffQ + tile * Y::kTile + tile_off(r, ch)) = w[ch];
-        fence_async_shared();
-    }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -241,23 +280,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicOr(a.status, PKV_STATUS_COPY_TIMEOUT);
         *stop_flag = 1;
     };
-    // ring item 2 jj is K of the jj-th tile, 2 jj + 1 its V
-    auto slot = [&](int it) { return it % Y::kStages; };
-    auto phase = [&](int it) { return static_cast<uint32_t>(it / Y::kStages) & 1u; };
-
     if (tile == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == kWarpLoad && lane == 0) {
-            int it = 0;
+            int it = early;
             for (; it < 2 * n && !stopped(); ++it) {
-                const int s = slot(it);
-                if (it >= Y::kStages && !wait_bar(bar(Y::kFree + s), phase(it - Y::kStages))) {
+                if (!wait_bar(bar(Y::kFree + slot(it)), phase(it - Y::kStages))) {
                     give_up();
                     break;
                 }
-                mbar_arrive_expect_tx(bar(Y::kFull + s), Y::kTile);
-                tma_load(sbase + Y::kOffRing + s * Y::kTile, it & 1 ? &vmap : &kmap, job.k0 + (js + it / 2) * kKeys, kvh,
-                         bar(Y::kFull + s));
+                load_item(it);
             }
             // stopping early: the copies in flight land (bounded) before the
             // shared memory is given up
@@ -530,14 +562,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            T* out = static_cast<T*>(a.out);
-#pragma unroll
+            constexpr int kStep = 32 / kCh;
+            const int ch = lane % kCh;
+            int rr = lane / kCh, orow_i = job.row0 + tile * kRows + (warp & 3) * 32 + rr;
+            int t = orow_i / a.G, hh = orow_i - t * a.G;
+            T* base = static_cast<T*>(a.out) + (static_cast<int64_t>(job.q0) * a.hq + kvh * a.G) * D + ch * 8;
+#pragma unroll 4
             for (int x = 0; x < kCh; ++x) {
-                const int idx = x * 32 + lane, rr = idx / kCh, ch = idx % kCh;
-                const int64_t dst = __shfl_sync(0xffffffffu, orow, rr);
-                const bool put = __shfl_sync(0xffffffffu, static_cast<int>(valid && ok), rr);
                 const uint4 w = *reinterpret_cast<const uint4*>(st + rr * (D * 2) + ((ch ^ (rr & 7)) << 4));
-                if (put) *reinterpret_cast<uint4*>(out + dst * D + ch * 8) = w;
+                if (ok && orow_i < job.rows)
+                    *reinterpret_cast<uint4*>(base + (static_cast<int64_t>(t) * a.hq + hh) * D) = w;
+                rr += kStep;
+                orow_i += kStep;
+                hh += kStep;
+                while (hh >= a.G) {
+                    hh -= a.G;
+                    ++t;
+                }
             }
         } else {
             const int64_t prow = static_cast<int64_t>(split) * a.T * a.hq + orow;
@@ -562,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == kWarpMma) {
         fence_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
