@@ -6,126 +6,882 @@
 // decode_quant.cu: (c - z) s for INT4, e4m3(c) s for FP8, 16-bit rows for
 // positions < n_sink and for the window blocks of the sequence ("The 8GB VRAM
 // Breakthrough", §4 with §6: the verify pass over the quantised cache).
-// One warp per (query token, query head) row: the lanes share the head dim,
-// the keys are taken one at a time with an online softmax in fp32.
+//
+// Up to 24 (query token, query head) rows per (sequence, KV head) -- gamma + 1
+// = 6 tokens at a GQA group of 4 -- take the balanced split of balanced.cuh:
+// warp i streams an equal share of the call's (sequence, KV head, 16-token
+// block) items and holds all rows of its runs, NT n-tiles of 8, so each code
+// is read and unpacked once for all of them; a merge kernel folds the partial
+// rows behind it.  More rows go to slice_quant.cu.
+//
+// The MMAs (mma.sync m16n8k16, tokens as M of QK^T, head dim as M of PV, rows
+// as N) see exact codes, the scales and zero points factored out:
+//   QK^T: S_t = s_t (sum_d q_d c_td - z_t sum_d q_d)
+//   PV:   O_d = sum_t W_t c_td - sum_t W_t z_t,  W_t = P_t s_t (fp16)
+// INT4 codes are used as fp16 subnormals (a nibble masked in place: c 2^-24,
+// the next nibble 16 c 2^-24; the query columns and outputs that meet the
+// latter are scaled to match), FP8 codes convert exactly.  sum_t W_t z_t is one
+// more MMA per n-tile: the zero points as a 17th row of V.
+// Sinks and window blocks are 16-bit blocks attended after the quantised ones
+// of a run, with the accumulator taken to true units first.
+//
+// Bound: HBM in bytes (1,088 per token and layer for 8 heads of INT4), in
+// practice the issue slots: ~290 instructions per block and KV head at 24
+// rows.  The next block's codes are loaded as soon as their registers are
+// free (K after QK^T, V after PV).
 
 #include <math.h>
 
 #include "balanced.cuh"
+#include "slice_quant.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int BS = 16;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;           // log2 units a logit may exceed the reference maximum by
+constexpr float kLazyMaxScale = 128.f;  // V scales above it take the exact maximum (W = P s stays in fp16)
+constexpr float kNoMax = -1e30f;        // reference maximum of a row that has seen no token
+constexpr float kTwo24 = 16777216.f;    // 2^24
+constexpr int kWarps = 2;               // warps per CTA
+constexpr int kMaxNT = 3;               // n-tiles of 8 rows per warp, at most
+// resident CTAs per SM, as the registers of NT n-tiles allow
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 6 : 4; }
+// Fewest items a warp takes: short runs cost a partial row set each, which
+// the merge reads back.
+constexpr int kMinItems = 8;
 
-struct MQQArgs {
-    const void* q;
-    const int32_t* q_start;
-    const uint8_t* codes[2];  // K, V
-    const __half* scale[2];
-    const __half* zero[2];
-    const void* sink[2];
-    const void* win[2];
-    int n_sink, window, ring;
-    const int32_t* tables;
-    const int32_t* ctx_lens;
-    int batch, hq, hkv, G, num_blocks, max_blocks, max_q_len;
-    float scale_log2;
-    void* out;
-    int* status;
+__device__ __forceinline__ uint32_t nib_even(uint32_t w) { return w & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t nib_odd(uint32_t w) { return w & 0x00F000F0u; }
+__device__ __forceinline__ uint32_t f16pair(float lo, float hi) { return Half16<__half>::pack(lo, hi); }
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    Half16<__half>::mma(d, a0, a1, a2, a3, b0, b1);
+}
+// two e4m3 codes in the low 16 bits of w -> fp16 pair
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {
+    uint32_t d;
+    const unsigned short a = static_cast<unsigned short>(w & 0xffffu);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(a));
+    return d;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ float half_at(const __half* p) { return __half2float(*p); }
+template <typename T>
+constexpr bool kSplitP = false;
+template <>
+constexpr bool kSplitP<__nv_bfloat16> = true;
+
+// The element of PV that m-tile mt, half hf (M rows g / g + 8) holds for lane
+// group g, and its head-dim column.  One column group per head: the lane
+// group's D / 8 consecutive columns; two groups of 64 (NG = 2): 8 columns of
+// each group, both halves of an m-tile in one group (its weights).
+template <int D, int NG>
+__host__ __device__ constexpr int pv_e(int mt, int hf) {
+    return NG == 1 ? mt + hf * (D / 16) : 8 * (mt / 4) + mt % 4 + 4 * hf;
+}
+template <int D, int NG>
+__device__ __forceinline__ int pv_column(int e, int g) {
+    return NG == 1 ? g * (D / 8) + e : (e >> 3) * 64 + 8 * g + (e & 7);
+}
+
+template <int D, int QMODE, int NG>
+struct Shape {
+    static constexpr bool INT4 = QMODE == PKV_QMODE_INT4_ASYM;
+    static constexpr int KSTEPS = D / 16;              // k-steps of QK^T
+    static constexpr int MT = D / 16;                  // m-tiles of PV
+    static constexpr int CB = INT4 ? D / 2 : D;        // code bytes per row
+    static constexpr int KW = INT4 ? D / 32 : D / 16;  // 32-bit K-code words per lane and row
+    static constexpr int VW = INT4 ? D / 64 : D / 32;  // 32-bit V-code words per lane and row
+    static constexpr int KPG = KW / NG, VPG = VW / NG;
+    static_assert(NG == 1 || (INT4 && D == 128 && NG == 2), "groups: one per head, or 64 columns at D 128");
 };
 
-// E consecutive values, from column col on, of the K (x = 0) or V (x = 1) row
-// at position t of sequence b; false on a bad table entry.
-template <typename T, int D, int QMODE, int E>
-__device__ __forceinline__ bool row_values(const MQQArgs& a, int x, int b, int kvh, int t, int w0, int group, int col,
-                                           float (&v)[E]) {
-    const T* src = nullptr;
-    if (t >= w0)
-        src = static_cast<const T*>(a.win[x]) +
-              (((static_cast<int64_t>(b) * a.ring + (t / BS) % a.ring) * a.hkv + kvh) * BS + t % BS) * D;
-    else if (t < a.n_sink)
-        src = static_cast<const T*>(a.sink[x]) + ((static_cast<int64_t>(b) * a.n_sink + t) * a.hkv + kvh) * D;
-    if (src) {
-        for (int e = 0; e < E; ++e) v[e] = Half16<T>::to_float(src[col + e]);
-        return true;
-    }
-    const int phys = a.tables[static_cast<int64_t>(b) * a.max_blocks + t / BS];
-    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.num_blocks)) return false;
-    const int64_t row = (static_cast<int64_t>(phys) * a.hkv + kvh) * BS + t % BS;
-    for (int e = 0; e < E; ++e) {
-        const int d = col + e;
-        if (QMODE == PKV_QMODE_INT4_ASYM) {
-            const int ng = D / group, gi = d / group;
-            const int c = (a.codes[x][row * (D / 2) + d / 2] >> (4 * (d & 1))) & 15;
-            v[e] = (c - __half2float(a.zero[x][row * ng + gi])) * __half2float(a.scale[x][row * ng + gi]);
+// One block's codes of a lane: K rows g, g + 8; V rows 2c, 2c + 1, 8 + 2c, 9 +
+// 2c.  kp / vp point at the lane's first bytes of the block's rows.
+template <int D, int QMODE, int NG>
+struct KCodes {
+    using S = Shape<D, QMODE, NG>;
+    uint32_t r0[S::KW], r1[S::KW];
+    __device__ __forceinline__ void load(const uint8_t* kp) {
+        if constexpr (!S::INT4) {
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) put<4>(4 * i, kp + 64 * i);
+        } else if constexpr (NG == 2) {
+            put<2>(0, kp);
+            put<2>(2, kp + 32);
         } else {
-            unsigned pair;
-            const unsigned short code = a.codes[x][row * D + d];
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"(code));
-            v[e] = __half2float(__ushort_as_half(static_cast<unsigned short>(pair & 0xffff))) *
-                   __half2float(a.scale[x][row]);
+            put<S::KW>(0, kp);
         }
     }
-    return true;
+    template <int N>
+    __device__ __forceinline__ void put(int at, const uint8_t* p) {
+        if constexpr (N == 4) {
+            const uint4 x = ldg_stream(p), y = ldg_stream(p + 8 * S::CB);
+            r0[at] = x.x; r0[at + 1] = x.y; r0[at + 2] = x.z; r0[at + 3] = x.w;
+            r1[at] = y.x; r1[at + 1] = y.y; r1[at + 2] = y.z; r1[at + 3] = y.w;
+        } else {
+            const uint2 x = ldg_stream8(p), y = ldg_stream8(p + 8 * S::CB);
+            r0[at] = x.x; r0[at + 1] = x.y;
+            r1[at] = y.x; r1[at + 1] = y.y;
+        }
+    }
+};
+
+template <int D, int QMODE, int NG>
+struct VCodes {
+    using S = Shape<D, QMODE, NG>;
+    uint32_t r[4][S::VW];
+    __device__ __forceinline__ void load(const uint8_t* vp) {
+        row(0, vp);
+        row(1, vp + S::CB);
+        row(2, vp + 8 * S::CB);
+        row(3, vp + 9 * S::CB);
+    }
+    __device__ __forceinline__ void row(int i, const uint8_t* p) {
+        if constexpr (NG == 2) {
+            r[i][0] = *reinterpret_cast<const uint32_t*>(p);
+            r[i][1] = *reinterpret_cast<const uint32_t*>(p + 32);
+        } else if constexpr (S::VW == 4) {
+            const uint4 x = ldg_stream(p);
+            r[i][0] = x.x; r[i][1] = x.y; r[i][2] = x.z; r[i][3] = x.w;
+        } else if constexpr (S::VW == 2) {
+            const uint2 x = ldg_stream8(p);
+            r[i][0] = x.x; r[i][1] = x.y;
+        } else {
+            r[i][0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+    }
+    // A fragment word: element e of token pair pr (rows 2 pr, 2 pr + 1)
+    __device__ __forceinline__ uint32_t frag(int e, int pr) const {
+        const uint32_t *a = r[2 * pr], *b = r[2 * pr + 1];
+        if constexpr (S::INT4) {
+            const int word = e >> 3, sub = (e >> 2) & 1, nib = e & 3;
+            const uint32_t x = __byte_perm(a[word], b[word], sub ? 0x7632u : 0x5410u);
+            const uint32_t y = nib >= 2 ? x >> 8 : x;
+            return (nib & 1) ? nib_odd(y) : nib_even(y);
+        } else {
+            const int word = e >> 2, sub = e & 3;
+            const uint32_t x = __byte_perm(a[word], b[word], (sub >> 1) ? 0x7362u : 0x5140u);
+            return e4m3x2((sub & 1) ? (x >> 16) : x);
+        }
+    }
+};
+
+// K scale / zero of tokens g, g + 8; V scale of the same tokens; V zero points
+// of tokens 2c, 2c + 1 and 8 + 2c, 9 + 2c as fragment words.
+template <int D, int QMODE, int NG>
+struct Scales {
+    __half2 ks[NG], vs[NG], kz[NG];  // low: token g, high: token g + 8
+    uint32_t vz[NG][2];
+    __device__ __forceinline__ void load(const QuantCache& a, int64_t row0, int g, int c) {
+        const int64_t s0 = (row0 + g) * NG;
+        const __half *k = a.scale[0] + s0, *v = a.scale[1] + s0;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            ks[i] = __halves2half2(k[i], k[8 * NG + i]);
+            vs[i] = __halves2half2(v[i], v[8 * NG + i]);
+        }
+        if constexpr (Shape<D, QMODE, NG>::INT4) {
+            const __half* kzp = a.zero[0] + s0;
+            const __half* z = a.zero[1] + (row0 + 2 * c) * NG;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) kz[i] = __halves2half2(kzp[i], kzp[8 * NG + i]);
+            if constexpr (NG == 1) {
+                vz[0][0] = *reinterpret_cast<const uint32_t*>(z);
+                vz[0][1] = *reinterpret_cast<const uint32_t*>(z + 8);
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(z), y = *reinterpret_cast<const uint2*>(z + 16);
+                vz[0][0] = __byte_perm(x.x, x.y, 0x5410u);
+                vz[NG - 1][0] = __byte_perm(x.x, x.y, 0x7632u);
+                vz[0][1] = __byte_perm(y.x, y.y, 0x5410u);
+                vz[NG - 1][1] = __byte_perm(y.x, y.y, 0x7632u);
+            }
+        }
+    }
+};
+
+// A warp's state over its run: lane (g, c) holds rows 8 nt + 2c, 8 nt + 2c + 1
+// of every n-tile.  corr: the zero-point MMA's accumulator (rows 0 and 8 of its
+// 16: column groups 0 and 1; lanes g = 0).
+template <int MT, int NT>
+struct State {
+    float m[NT][2], l[NT][2];
+    float o[MT][NT][4];
+    float corr[NT][4];
+};
+
+// Raises the reference maxima to cover the logits x (of all n-tiles) and
+// rescales what was accumulated against the old ones.
+template <int MT, int NT>
+__device__ __forceinline__ void raise_max(State<MT, NT>& w, const float (&x)[NT][4]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float b = fmaxf(x[nt][k], x[nt][k + 2]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
+            const float mn = fmaxf(w.m[nt][k], b);
+            const float al = ex2(w.m[nt][k] - mn);
+            w.m[nt][k] = mn;
+            w.l[nt][k] *= al;
+            w.corr[nt][k] *= al;
+            w.corr[nt][k + 2] *= al;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                w.o[mt][nt][k] *= al;
+                w.o[mt][nt][k + 2] *= al;
+            }
+        }
+    }
 }
 
-template <typename T, int D, int QMODE>
-__global__ void mqq_rows_kernel(MQQArgs a, int group) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int h = blockIdx.y, b = blockIdx.z, kvh = h / a.G;
-    const int q0 = a.q_start[b], L = a.q_start[b + 1] - q0;
+// Adds V's non-finite values v(t, column) of tokens [t0, t1) to the rows that
+// see them; the MMA was given zeros in their place (0 x NaN would have reached
+// the rows that do not).
+template <int D, int NG, int NT, typename V>
+__device__ __forceinline__ void add_non_finite(State<D / 16, NT>& w, const int (&pos)[NT][2], int t0, int t1, int g, V v) {
+    for (int t = t0; t < t1; ++t) {
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const float x = v(t, pv_column<D, NG>(pv_e<D, NG>(mt, hf), g));
+                if (fabsf(x) <= 3.4e38f) continue;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (t <= pos[nt][0]) w.o[mt][nt][2 * hf] += x;
+                    if (t <= pos[nt][1]) w.o[mt][nt][2 * hf + 1] += x;
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int D, int QMODE, int NG, int NT>
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
+    mqq_balanced_kernel(const __grid_constant__ QuantCache a, int nwt_launch, float* ws_o, float* ws_ml) {
+    using S = Shape<D, QMODE, NG>;
+    constexpr int KW = S::KW, MT = S::MT, R = 8 * NT, QW = S::KSTEPS / 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;");
+    // per warp: the run's query fragments ([NT][QW][32] uint4) while it
+    // attends, then its R x D partial outputs
+    static_assert(R * D >= NT * QW * 32 * 4, "slice too small for the query fragments");
+    __shared__ __align__(16) float slice[kWarps][R * D];
+    uint4* sq = reinterpret_cast<uint4*>(&slice[warp][0]) + lane;
+    const uint32_t qs_addr = static_cast<uint32_t>(__cvta_generic_to_shared(sq));
+
+    const int i = blockIdx.x * kWarps + warp;
     const int cap = a.max_blocks * BS;
-    int ctx = a.ctx_lens[b];
-    if (L <= 0 || i >= min(L, a.max_q_len)) return;
-    if ((ctx < L || ctx > cap || L > a.max_q_len) && lane == 0 && h == 0 && i == 0)
-        atomicOr(a.status, PKV_STATUS_BAD_CONTEXT);
-    ctx = min(max(ctx, 0), cap);
-    const int pos = ctx - L + i;
-    const int w0 = a.window > 0 ? max(ctx - a.window, 0) / BS * BS : ctx;
-    const T* q = static_cast<const T*>(a.q) + ((static_cast<int64_t>(q0) + i) * a.hq + h) * D + lane * E;
-    float x[E], o[E], m = neg_inf(), l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        x[e] = Half16<T>::to_float(q[e]);
-        o[e] = 0.f;
-    }
-    for (int t = 0; t <= pos; ++t) {
-        float v[E];
-        if (!row_values<T, D, QMODE, E>(a, 0, b, kvh, t, w0, group, lane * E, v)) {
-            if (lane == 0) atomicOr(a.status, PKV_STATUS_BAD_BLOCK);
-            continue;
+    WarpSplit sp;
+    bool bad = false;
+    const bool any = sp.begin(a.ctx_lens, a.batch, cap, a.hkv, nwt_launch, kMinItems, i, bad);
+    if (i == 0 && bad && lane == 0) atomicOr(a.status, PKV_STATUS_BAD_CONTEXT);
+    if (!any) return;
+    while (sp.next()) {
+        const int b = sp.b, kvh = sp.kvh, ctx = sp.ctx;
+        const int q0 = a.q_start[b], L = a.q_start[b + 1] - q0;
+        if (L <= 0) continue;
+        const int rows = min(L, a.max_q_len) * a.G;
+        if ((L > a.max_q_len || ctx < L) && lane == 0 && sp.lb0 == 0 && kvh == 0)
+            atomicOr(a.status, PKV_STATUS_BAD_CONTEXT);
+        const int first_pos = ctx - L;
+        const T* qbase = static_cast<const T*>(a.q) + (static_cast<int64_t>(q0) * a.hq + kvh * a.G) * D;
+        auto qrow = [&](int row) {
+            const int tok = row / a.G;
+            return qbase + (static_cast<int64_t>(tok) * a.hq + (row - tok * a.G)) * D;
+        };
+
+        // ---- query fragments in fp16, in the k order of the codes, and the
+        // rows' sums per column group
+        float qs[NT][NG][2];
+        __syncwarp();  // the previous run's partial rows have been copied out
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = 8 * nt + g;
+            const bool valid = row < rows;
+            const T* q = qrow(valid ? row : 0);
+            float sum[NG];
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) sum[gi] = 0.f;
+#pragma unroll
+            for (int k = 0; k < QW; ++k) {
+                // INT4: word k covers 8 columns; FP8: 8 columns of load k / 2
+                const int col = S::INT4 ? (k / S::KPG) * (D / NG) + (D / NG / 4) * c + 8 * (k % S::KPG)
+                                        : 64 * (k / 2) + 16 * c + 8 * (k % 2);
+                const uint4 raw = valid ? *reinterpret_cast<const uint4*>(q + col) : make_uint4(0, 0, 0, 0);
+                const T* e = reinterpret_cast<const T*>(&raw);
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    // fp16, saturating, as the MMA sees it
+                    x[j] = __half2float(__float2half_rn(fminf(fmaxf(Half16<T>::to_float(e[j]), -65504.f), 65504.f)));
+                    if (Half16<T>::to_float(e[j]) != Half16<T>::to_float(e[j])) x[j] = Half16<T>::to_float(e[j]);
+                    sum[S::INT4 ? k / S::KPG : 0] += x[j];
+                }
+                uint4 f;
+                if constexpr (S::INT4) {
+                    // k-step 2k: nibbles {0, 4} and {1, 5}; 2k + 1: {2, 6}, {3, 7}; the
+                    // odd nibbles enter 16 x larger
+                    f.x = f16pair(x[0], x[4]);
+                    f.y = f16pair(x[1] * 0.0625f, x[5] * 0.0625f);
+                    f.z = f16pair(x[2], x[6]);
+                    f.w = f16pair(x[3] * 0.0625f, x[7] * 0.0625f);
+                } else {
+                    f.x = f16pair(x[0], x[1]);
+                    f.y = f16pair(x[2], x[3]);
+                    f.z = f16pair(x[4], x[5]);
+                    f.w = f16pair(x[6], x[7]);
+                }
+                sq[(nt * QW + k) * 32] = f;
+            }
+            if constexpr (S::INT4) {
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 1);
+                    sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 2);
+                    qs[nt][gi][0] = __shfl_sync(0xffffffffu, sum[gi], 8 * c);
+                    qs[nt][gi][1] = __shfl_sync(0xffffffffu, sum[gi], 8 * c + 4);
+                }
+            }
         }
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += x[e] * v[e];
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= a.scale_log2;
-        if (s == neg_inf()) continue;
-        const float mn = fmaxf(m, s);
-        const float al = ex2(m - mn), p = ex2(s - mn);
-        m = mn;
-        l = l * al + p;
-        row_values<T, D, QMODE, E>(a, 1, b, kvh, t, w0, group, lane * E, v);
-        for (int e = 0; e < E; ++e) o[e] = o[e] * al + p * v[e];
+        __syncwarp();
+        int pos[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int row = 8 * nt + 2 * c + k;
+                const int p = row < rows ? first_pos + row / a.G : -1;
+                pos[nt][k] = p < 0 ? -1 : p;
+            }
+        }
+        State<MT, NT> w;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            w.m[nt][0] = w.m[nt][1] = kNoMax;
+            w.l[nt][0] = w.l[nt][1] = 0.f;
+            w.corr[nt][0] = w.corr[nt][1] = w.corr[nt][2] = w.corr[nt][3] = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) w.o[mt][nt][0] = w.o[mt][nt][1] = w.o[mt][nt][2] = w.o[mt][nt][3] = 0.f;
+        }
+        // window blocks start at win_lb; block 0's first n_sink tokens are sinks
+        const int win_lb = a.window > 0 ? max(ctx - a.window, 0) / BS : 0x7fffffff;
+        const int q_end = min(sp.lb1, win_lb);
+        const int sinks = win_lb > 0 ? a.n_sink : 0;
+        // blocks below full_lb are seen whole by every row (rows that do not
+        // exist aside: their outputs go nowhere)
+        const int full_lb = max(first_pos + 1, 0) / BS;
+
+        // ---- quantised blocks
+        const uint8_t* kbase = a.codes[0] + g * S::CB +
+                               (!S::INT4 ? 16 * c : NG == 2 ? 8 * c : (KW == 4 ? 16 * c : 8 * c));
+        const uint8_t* vbase = a.codes[1] + 2 * c * S::CB + (S::INT4 ? (NG == 2 ? 4 * g : D / 16 * g) : D / 8 * g);
+        const int32_t* trow = a.tables + static_cast<int64_t>(b) * a.max_blocks;
+        auto row0_of = [&](int phys) { return (static_cast<int64_t>(phys) * a.hkv + kvh) * BS; };
+        auto valid = [&](int phys) { return static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks); };
+        int tab = sp.lb0 + lane < q_end ? trow[sp.lb0 + lane] : -1;
+        int phys = __shfl_sync(0xffffffffu, tab, 0);
+        KCodes<D, QMODE, NG> kc;
+        VCodes<D, QMODE, NG> vc;
+        Scales<D, QMODE, NG> sc;
+        if (sp.lb0 < q_end && valid(phys)) {
+            kc.load(kbase + row0_of(phys) * S::CB);
+            vc.load(vbase + row0_of(phys) * S::CB);
+            sc.load(a, row0_of(phys), g, c);
+        }
+        for (int lb = sp.lb0, k = 0; lb < q_end; ++lb, ++k) {
+            int pn = -1;
+            if (lb + 1 < q_end) {
+                if (((k + 1) & 31) == 0) {  // ids of the run's next 32 blocks
+                    const int idx = lb + 1 + lane;
+                    tab = idx < q_end ? trow[idx] : -1;
+                }
+                pn = __shfl_sync(0xffffffffu, tab, (k + 1) & 31);
+            }
+            const bool nv = valid(pn);
+            if (!valid(phys)) {
+                if (lane == 0) atomicOr(a.status, PKV_STATUS_BAD_BLOCK);
+                if (nv) {  // nothing attended: fetch the next block now
+                    kc.load(kbase + row0_of(pn) * S::CB);
+                    vc.load(vbase + row0_of(pn) * S::CB);
+                    sc.load(a, row0_of(pn), g, c);
+                }
+                phys = pn;
+                continue;
+            }
+            // ---- S^T = C Q^T over the code values, per column group
+            float s[NG][NT][4];
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[gi][nt][0] = s[gi][nt][1] = s[gi][nt][2] = s[gi][nt][3] = 0.f;
+#pragma unroll
+            for (int t = 0; t < QW; ++t) {
+                uint32_t f[8];
+                if constexpr (S::INT4) {
+                    const uint32_t u0 = kc.r0[t] >> 8, u1 = kc.r1[t] >> 8;
+                    f[0] = nib_even(kc.r0[t]); f[1] = nib_even(kc.r1[t]); f[2] = nib_odd(kc.r0[t]); f[3] = nib_odd(kc.r1[t]);
+                    f[4] = nib_even(u0); f[5] = nib_even(u1); f[6] = nib_odd(u0); f[7] = nib_odd(u1);
+                } else {
+                    const int j = 2 * t;  // k-steps 2t, 2t + 1 use words 2t, 2t + 1
+                    f[0] = e4m3x2(kc.r0[j]); f[1] = e4m3x2(kc.r1[j]); f[2] = e4m3x2(kc.r0[j] >> 16); f[3] = e4m3x2(kc.r1[j] >> 16);
+                    f[4] = e4m3x2(kc.r0[j + 1]); f[5] = e4m3x2(kc.r1[j + 1]);
+                    f[6] = e4m3x2(kc.r0[j + 1] >> 16); f[7] = e4m3x2(kc.r1[j + 1] >> 16);
+                }
+                const int gi = S::INT4 ? t / S::KPG : 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 q = lds128(qs_addr + (nt * QW + t) * 512);
+                    mma_f16(s[gi][nt], f[0], f[1], f[2], f[3], q.x, q.y);
+                    mma_f16(s[gi][nt], f[4], f[5], f[6], f[7], q.z, q.w);
+                }
+            }
+            if (nv) kc.load(kbase + row0_of(pn) * S::CB);
+
+            // ---- logits (base 2)
+            float x[NT][4];
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) {
+                const float k0 = __low2float(sc.ks[gi]) * a.scale_log2, k1 = __high2float(sc.ks[gi]) * a.scale_log2;
+                float z0 = 0.f, z1 = 0.f;
+                if constexpr (S::INT4) {
+                    z0 = -k0 * __low2float(sc.kz[gi]);
+                    z1 = -k1 * __high2float(sc.kz[gi]);
+                }
+                const float m0 = S::INT4 ? k0 * kTwo24 : k0, m1 = S::INT4 ? k1 * kTwo24 : k1;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float sv = s[gi][nt][j], mul = j < 2 ? m0 : m1;
+                        float y = gi == 0 ? sv * mul : fmaf(sv, mul, x[nt][j]);
+                        if constexpr (S::INT4) y = fmaf(j < 2 ? z0 : z1, qs[nt][gi][j & 1], y);
+                        x[nt][j] = y;
+                    }
+                }
+            }
+            const int t0 = lb * BS;
+            const bool masked = lb >= full_lb || (lb == 0 && sinks > 0);
+            bool fix_nan = false;
+            float vs0[NG], vs1[NG];
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) {
+                vs0[gi] = __low2float(sc.vs[gi]);
+                vs1[gi] = __high2float(sc.vs[gi]);
+            }
+            if (masked) {
+                const bool in0 = t0 + g < ctx && t0 + g >= sinks, in1 = t0 + g + 8 < ctx && t0 + g + 8 >= sinks;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        if (!in0 || t0 + g > pos[nt][k2]) x[nt][k2] = neg_inf();
+                        if (!in1 || t0 + g + 8 > pos[nt][k2]) x[nt][k2 + 2] = neg_inf();
+                    }
+                }
+                // slots that hold no token, and sinks: any bits; their weight is
+                // 0, their scale and zero point are taken out
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    if (!in0) vs0[gi] = 0.f;
+                    if (!in1) vs1[gi] = 0.f;
+                    if constexpr (S::INT4) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int t = t0 + 2 * c + 8 * hf;
+                            if (t >= ctx || t < sinks) sc.vz[gi][hf] &= 0xffff0000u;
+                            if (t + 1 >= ctx || t + 1 < sinks) sc.vz[gi][hf] &= 0x0000ffffu;
+                        }
+                    }
+                }
+                if constexpr (!S::INT4) {
+                    // codes of slots without a token, and NaN codes
+                    bool odd = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = t0 + 2 * c + (j & 1) + 8 * (j >> 1);
+#pragma unroll
+                        for (int v = 0; v < S::VW; ++v) {
+                            if (t >= ctx || t < sinks) vc.r[j][v] = 0;
+                            const uint32_t nan = __vcmpeq4(vc.r[j][v] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            odd |= nan != 0;
+                            vc.r[j][v] &= ~nan;
+                        }
+                    }
+                    fix_nan = __any_sync(0xffffffffu, odd);
+                }
+            }
+
+            // ---- online softmax: the reference maxima move only when a logit
+            // exceeds them by more than kSlack, or a V scale is large
+            bool up = false;
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) up |= fmaxf(vs0[gi], vs1[gi]) > kLazyMaxScale;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                up |= fmaxf(x[nt][0], x[nt][2]) > w.m[nt][0] + kSlack;
+                up |= fmaxf(x[nt][1], x[nt][3]) > w.m[nt][1] + kSlack;
+            }
+            if (__any_sync(0xffffffffu, up)) raise_max<MT, NT>(w, x);
+            uint32_t b0[NG][NT], b1[NG][NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float p0 = ex2(x[nt][0] - w.m[nt][0]), p1 = ex2(x[nt][1] - w.m[nt][1]);
+                const float p2 = ex2(x[nt][2] - w.m[nt][0]), p3 = ex2(x[nt][3] - w.m[nt][1]);
+                w.l[nt][0] += p0 + p2;
+                w.l[nt][1] += p1 + p3;
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    b0[gi][nt] = movmatrix_trans(f16pair(p0 * vs0[gi], p1 * vs0[gi]));
+                    b1[gi][nt] = movmatrix_trans(f16pair(p2 * vs1[gi], p3 * vs1[gi]));
+                }
+            }
+            // ---- sum_t W_t z_t: zero points as row 0 (group 0) and 8 (group 1)
+            if constexpr (S::INT4) {
+                const uint32_t on = g == 0 ? 0xffffffffu : 0u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(w.corr[nt], sc.vz[0][0] & on, 0u, sc.vz[0][1] & on, 0u, b0[0][nt], b1[0][nt]);
+                    if constexpr (NG == 2)
+                        mma_f16(w.corr[nt], 0u, sc.vz[NG - 1][0] & on, 0u, sc.vz[NG - 1][1] & on, b0[NG - 1][nt],
+                                b1[NG - 1][nt]);
+                }
+            }
+            if (nv) sc.load(a, row0_of(pn), g, c);
+            // ---- O^T += C_v^T W^T
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int el = pv_e<D, NG>(mt, 0), eh = pv_e<D, NG>(mt, 1);
+                const uint32_t f0 = vc.frag(el, 0), f1 = vc.frag(eh, 0), f2 = vc.frag(el, 1), f3 = vc.frag(eh, 1);
+                const int gi = S::INT4 ? (el >> 3) / S::VPG : 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(w.o[mt][nt], f0, f1, f2, f3, b0[gi][nt], b1[gi][nt]);
+            }
+            if constexpr (!S::INT4) {
+                if (fix_nan) {
+                    const uint8_t* codes = a.codes[1] + row0_of(phys) * S::CB;
+                    add_non_finite<D, NG, NT>(w, pos, max(t0, sinks), min(t0 + BS, ctx), g, [&](int t, int col) {
+                        return (codes[(t - t0) * S::CB + col] & 0x7f) == 0x7f ? __int_as_float(0x7fc00000) : 0.f;
+                    });
+                }
+            }
+            if (nv) vc.load(vbase + row0_of(pn) * S::CB);
+            phys = pn;
+        }
+
+        // ---- to true units: INT4 products are in 2^-24 (odd nibbles 2^-20),
+        // and the zero points come off
+        if constexpr (S::INT4) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float cr[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cr[j] = __shfl_sync(0xffffffffu, w.corr[nt][j], c);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int el = pv_e<D, NG>(mt, 0);
+                    const int gi = (el >> 3) / S::VPG;
+                    const float u = (el & 1) ? kTwo24 * 0.0625f : kTwo24;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w.o[mt][nt][j] = fmaf(w.o[mt][nt][j], u, -cr[2 * gi + (j & 1)]);
+                }
+            }
+        }
+
+        // ---- 16-bit blocks: the sinks (their rows stand in for block 0's first
+        // n_sink tokens), then the window.  kr / vr: row 0, rows apart by
+        // `stride`; tokens t0 .. t0 + n - 1.
+        auto attend16 = [&](const T* kr, const T* vr, int64_t stride, int t0, int n) {
+            using H = Half16<T>;
+            constexpr int KC = D / 32, VC = D / 64;
+            auto at = [&](int r) { return min(r, n - 1) * stride; };  // never past the last row
+            float x[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KC; ++k) {
+                const uint4 k0 = ldg_stream(kr + at(g) + 32 * k + 8 * c), k1 = ldg_stream(kr + at(g + 8) + 32 * k + 8 * c);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int row = 8 * nt + g;
+                    const uint4 q = row < rows ? *reinterpret_cast<const uint4*>(qrow(row) + 32 * k + 8 * c)
+                                               : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        H::mma(x[nt], word(k0, 2 * e), word(k1, 2 * e), word(k0, 2 * e + 1), word(k1, 2 * e + 1),
+                               word(q, 2 * e), word(q, 2 * e + 1));
+                }
+            }
+            bool up = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = g + 8 * (j >> 1);
+                    x[nt][j] = r < n && t0 + r <= pos[nt][j & 1] ? x[nt][j] * a.scale_log2 : neg_inf();
+                    up |= x[nt][j] > w.m[nt][j & 1] + kSlack;
+                }
+            }
+            if (__any_sync(0xffffffffu, up)) raise_max<MT, NT>(w, x);
+            uint32_t b0[NT], b1[NT], e0[NT], e1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float p0 = ex2(x[nt][0] - w.m[nt][0]), p1 = ex2(x[nt][1] - w.m[nt][1]);
+                const float p2 = ex2(x[nt][2] - w.m[nt][0]), p3 = ex2(x[nt][3] - w.m[nt][1]);
+                w.l[nt][0] += p0 + p2;
+                w.l[nt][1] += p1 + p3;
+                const uint32_t h01 = H::pack(p0, p1), h23 = H::pack(p2, p3);
+                b0[nt] = movmatrix_trans(h01);
+                b1[nt] = movmatrix_trans(h23);
+                if constexpr (kSplitP<T>) {  // bf16 P goes in as value and rounding residual
+                    e0[nt] = movmatrix_trans(H::pack(p0 - __uint_as_float(h01 << 16), p1 - __uint_as_float(h01 & 0xffff0000u)));
+                    e1[nt] = movmatrix_trans(H::pack(p2 - __uint_as_float(h23 << 16), p3 - __uint_as_float(h23 & 0xffff0000u)));
+                }
+            }
+            uint4 v[4][VC];
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 2 * c + (j & 1) + 8 * (j >> 1);
+#pragma unroll
+                for (int x2 = 0; x2 < VC; ++x2) {
+                    v[j][x2] = r < n ? ldg_stream(vr + at(r) + (NG == 2 ? 64 * x2 + 8 * g : g * (D / 8) + 8 * x2))
+                                     : make_uint4(0, 0, 0, 0);
+                    // non-finite values: out of the product (see add_non_finite)
+                    constexpr uint32_t kExp = kSplitP<T> ? 0x7F80u : 0x7C00u;
+                    uint32_t* wd = reinterpret_cast<uint32_t*>(&v[j][x2]);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        if ((wd[y] & kExp) == kExp) { wd[y] &= 0xffff0000u; odd = true; }
+                        if (((wd[y] >> 16) & kExp) == kExp) { wd[y] &= 0x0000ffffu; odd = true; }
+                    }
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                uint32_t f[4];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int e = pv_e<D, NG>(mt, hf), ch = e >> 3, wd = (e & 7) >> 1;
+                    const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+                    f[hf] = __byte_perm(word(v[0][ch], wd), word(v[1][ch], wd), sel);
+                    f[hf + 2] = __byte_perm(word(v[2][ch], wd), word(v[3][ch], wd), sel);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    H::mma(w.o[mt][nt], f[0], f[1], f[2], f[3], b0[nt], b1[nt]);
+                    if constexpr (kSplitP<T>) H::mma(w.o[mt][nt], f[0], f[1], f[2], f[3], e0[nt], e1[nt]);
+                }
+            }
+            if (__any_sync(0xffffffffu, odd))
+                add_non_finite<D, NG, NT>(w, pos, t0, t0 + n, g, [&](int t, int col) {
+                    const float x2 = Half16<T>::to_float(vr[(t - t0) * stride + col]);
+                    return x2;
+                });
+        };
+        if (sp.lb0 == 0 && sinks > 0) {
+            const int64_t at = (static_cast<int64_t>(b) * a.n_sink * a.hkv + kvh) * D;
+            const int n = min(sinks, ctx);
+            if (n > 0)
+                attend16(static_cast<const T*>(a.sink[0]) + at, static_cast<const T*>(a.sink[1]) + at,
+                         static_cast<int64_t>(a.hkv) * D, 0, n);
+        }
+        for (int lb = max(sp.lb0, win_lb); lb < sp.lb1; ++lb) {
+            const int64_t at = ((static_cast<int64_t>(b) * a.ring + lb % a.ring) * a.hkv + kvh) * (BS * D);
+            attend16(static_cast<const T*>(a.win[0]) + at, static_cast<const T*>(a.win[1]) + at, D, lb * BS,
+                     min(BS, ctx - lb * BS));
+        }
+
+        // ---- the run's partial rows: l totalled over the token lanes, o
+        // staged through the slice so rows go out in 16-byte stores
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                w.l[nt][0] += __shfl_xor_sync(0xffffffffu, w.l[nt][0], off);
+                w.l[nt][1] += __shfl_xor_sync(0xffffffffu, w.l[nt][1], off);
+            }
+        }
+        __syncwarp();  // the query fragments are no longer read
+        float* so = &slice[warp][0];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = pv_column<D, NG>(pv_e<D, NG>(mt, j >> 1), g);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) so[(8 * nt + 2 * c + (j & 1)) * D + d] = w.o[mt][nt][j];
+            }
+        }
+        __syncwarp();
+        const int64_t slot = i + static_cast<int64_t>(b) * a.hkv + kvh;
+        float4* po = reinterpret_cast<float4*>(ws_o + slot * R * D);
+        const float4* s4 = reinterpret_cast<const float4*>(so);
+        for (int y = lane; y < rows * D / 4; y += 32) po[y] = s4[y];
+        if (g == 0) {
+            float* pml = ws_ml + slot * R * 2;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int row = 8 * nt + 2 * c + k;
+                    if (row < rows) *reinterpret_cast<float2*>(pml + 2 * row) = make_float2(w.m[nt][k], w.l[nt][k]);
+                }
+            }
+        }
     }
-    T* out = static_cast<T*>(a.out) + ((static_cast<int64_t>(q0) + i) * a.hq + h) * D + lane * E;
-    for (int e = 0; e < E; ++e) out[e] = Half16<T>::from_float(l > 0.f || l != l ? o[e] / l : 0.f);
 }
 
-template <typename T, int D, int QMODE>
-void launch_rows(const MQQArgs& a, int group, cudaStream_t st) {
-    mqq_rows_kernel<T, D, QMODE><<<dim3((a.max_q_len + 3) / 4, a.hq, a.batch), 128, 0, st>>>(a, group);
+// Merge of the partial rows: one CTA per (8 rows, KV head, sequence), a warp
+// per row, lanes over the head dim (and, for the weights, over the partials).
+// Where the run's partials sit follows from the context lengths alone, so it
+// is worked out before the wait on the split grid.
+constexpr int kMergeWarps = 8;
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    mqq_merge_kernel(const __grid_constant__ QuantCache a, int nwt_launch, const float* __restrict__ ws_o,
+                     const float* __restrict__ ws_ml) {
+    constexpr int R = 8 * NT, E = D / 32;
+    const int kvh = blockIdx.x / NT, r = blockIdx.x % NT * 8 + (threadIdx.x >> 5), b = blockIdx.y;
+    const int lane = threadIdx.x & 31, cap = a.max_blocks * BS;
+    int before = 0, total = 0;
+    for (int j = lane; j < a.batch; j += 32) {
+        const int nbj = blocks_of(a.ctx_lens[j], cap);
+        total += nbj;
+        before += j < b ? nbj : 0;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    const int q0 = a.q_start[b], L = a.q_start[b + 1] - q0;
+    const int rows = L > 0 ? min(L, a.max_q_len) * a.G : 0;
+    const int nb = blocks_of(a.ctx_lens[b], cap);
+    const int W = total * a.hkv;
+    const int nwt = max(min(W / kMinItems, nwt_launch), 1);
+    int64_t slot0 = 0;
+    int np = 0;
+    if (nb > 0) {
+        const int at = before * a.hkv + kvh * nb;
+        const int64_t i0 = first_warp(at, W, nwt), i1 = first_warp(at + nb - 1, W, nwt);
+        slot0 = i0 + static_cast<int64_t>(b) * a.hkv + kvh;
+        np = static_cast<int>(i1 - i0 + 1);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (r >= rows) return;
+    const float2* ml = reinterpret_cast<const float2*>(ws_ml) + slot0 * R + r;  // partial p: ml[p R]
+    const float* po = ws_o + (slot0 * R + r) * D + lane * E;
+    float M = kNoMax;
+    for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(ml + static_cast<int64_t>(p) * R).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float Ls = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int p0 = 0; p0 < np; p0 += 32) {
+        float wt = 0.f;
+        if (p0 + lane < np) {
+            const float2 v = __ldcg(ml + static_cast<int64_t>(p0 + lane) * R);
+            wt = ex2(v.x - M);
+            Ls += wt * v.y;
+        }
+        const int n = min(32, np - p0);
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+            const float f = __shfl_sync(0xffffffffu, wt, j);
+            const float* p = po + static_cast<int64_t>(p0 + j) * R * D;
+            if constexpr (E == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+                o[0] += f * v.x;
+                o[1] += f * v.y;
+                o[2] += f * v.z;
+                o[3] += f * v.w;
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+                o[0] += f * v.x;
+                o[1] += f * v.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, off);
+    const float inv = Ls > 0.f ? 1.f / Ls : (Ls == 0.f ? 0.f : Ls);  // NaN stays
+    const int tok = r / a.G;
+    T* dst = static_cast<T*>(a.out) +
+             ((static_cast<int64_t>(q0) + tok) * a.hq + kvh * a.G + (r - tok * a.G)) * D + lane * E;
+    uint32_t v[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) v[e] = Ls == 0.f ? 0u : Half16<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = v[0];
+}
+
+// n-tiles of the balanced split for rows per (sequence, KV head), 0: too many
+// rows (or too many items to index).
+int small_nt(int64_t batch, int64_t hkv, int64_t max_blocks, int64_t rows) {
+    if (rows > 8 * kMaxNT || batch * hkv * max_blocks >= (1LL << 30)) return 0;
+    return rows <= 0 ? 1 : static_cast<int>((rows + 7) / 8);
+}
+
+// Warps the split launches: all resident at once, kMinItems items each.
+int small_warps(int64_t items, int nt) {
+    const int64_t full = static_cast<int64_t>(num_sms()) * kWarps * ctas_per_sm(nt);
+    const int64_t n = items / kMinItems;
+    return static_cast<int>(n < 1 ? 1 : (n > full ? full : n));
+}
+
+size_t small_bytes(int64_t batch, int64_t hkv, int D, int nt, int nwt) {
+    return static_cast<size_t>(nwt + batch * hkv) * 8 * nt * (D + 2) * sizeof(float);
+}
+
+template <typename T, int D, int QMODE, int NG, int NT>
+int run_small(const QuantCache& a, int nwt, float* ws_o, float* ws_ml, cudaStream_t st) {
+    mqq_balanced_kernel<T, D, QMODE, NG, NT><<<(nwt + kWarps - 1) / kWarps, kWarps * 32, 0, st>>>(a, nwt, ws_o, ws_ml);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.hkv * NT, a.batch);
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mqq_merge_kernel<T, D, NT>, a, nwt, static_cast<const float*>(ws_o),
+                              static_cast<const float*>(ws_ml)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+template <typename T, int D, int QMODE, int NG>
+int run_small_nt(const QuantCache& a, int nt, int nwt, float* ws_o, float* ws_ml, cudaStream_t st) {
+    if (nt == 1) return run_small<T, D, QMODE, NG, 1>(a, nwt, ws_o, ws_ml, st);
+    if (nt == 2) return run_small<T, D, QMODE, NG, 2>(a, nwt, ws_o, ws_ml, st);
+    return run_small<T, D, QMODE, NG, 3>(a, nwt, ws_o, ws_ml, st);
 }
 
 template <typename T>
-void launch_rows_t(const MQQArgs& a, int D, int qmode, int group, cudaStream_t st) {
-    const bool int4 = qmode == PKV_QMODE_INT4_ASYM;
-    if (D == 128 && int4) launch_rows<T, 128, PKV_QMODE_INT4_ASYM>(a, group, st);
-    else if (D == 128) launch_rows<T, 128, PKV_QMODE_FP8_E4M3>(a, group, st);
-    else if (int4) launch_rows<T, 64, PKV_QMODE_INT4_ASYM>(a, group, st);
-    else launch_rows<T, 64, PKV_QMODE_FP8_E4M3>(a, group, st);
+int run_small_t(const QuantCache& a, int D, int nt, int nwt, float* ws_o, float* ws_ml, cudaStream_t st) {
+    if (a.int4) {
+        if (D == 64) return run_small_nt<T, 64, PKV_QMODE_INT4_ASYM, 1>(a, nt, nwt, ws_o, ws_ml, st);
+        if (a.groups == 2) return run_small_nt<T, 128, PKV_QMODE_INT4_ASYM, 2>(a, nt, nwt, ws_o, ws_ml, st);
+        return run_small_nt<T, 128, PKV_QMODE_INT4_ASYM, 1>(a, nt, nwt, ws_o, ws_ml, st);
+    }
+    if (D == 64) return run_small_nt<T, 64, PKV_QMODE_FP8_E4M3, 1>(a, nt, nwt, ws_o, ws_ml, st);
+    return run_small_nt<T, 128, PKV_QMODE_FP8_E4M3, 1>(a, nt, nwt, ws_o, ws_ml, st);
 }
 
 }  // namespace
@@ -138,7 +894,16 @@ extern "C" int pkv_multi_query_quant_workspace_bytes(int32_t batch, int32_t num_
         block_size <= 0 || max_q_len < 0 || num_q_heads % num_kv_heads != 0)
         return PKV_ERR_INVALID_ARG;
     if (block_size != pkv::BS) return PKV_ERR_UNSUPPORTED;
-    *out = 0;
+    const int64_t rows = static_cast<int64_t>(max_q_len) * (num_q_heads / num_kv_heads);
+    const int nt = pkv::small_nt(batch, num_kv_heads, max_blocks, rows);
+    if (batch == 0 || max_q_len == 0) {
+        *out = 0;
+    } else if (nt > 0) {
+        const int nwt = pkv::small_warps(static_cast<int64_t>(batch) * num_kv_heads * max_blocks, nt);
+        *out = pkv::small_bytes(batch, num_kv_heads, head_dim, nt, nwt);
+    } else {
+        *out = pkv::slice_quant_workspace(batch, num_q_heads, num_kv_heads, head_dim, max_blocks, max_q_len);
+    }
     return PKV_OK;
 }
 
@@ -175,7 +940,13 @@ extern "C" int pkv_paged_attention_multi_query_quant(
         return PKV_ERR_MISALIGNED;
     int* st = pkv::status_word();
     if (!st) return PKV_ERR_CUDA;
-    pkv::MQQArgs a;
+    size_t need = 0;
+    const int rc = pkv_multi_query_quant_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_blocks,
+                                                         block_size, max_q_len, &need);
+    if (rc != PKV_OK) return rc;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return PKV_ERR_WORKSPACE;
+    if (need > 0 && !pkv::aligned16(workspace)) return PKV_ERR_MISALIGNED;
+    pkv::QuantCache a;
     a.q = q;
     a.q_start = q_start;
     a.codes[0] = static_cast<const uint8_t*>(k_codes);
@@ -200,11 +971,18 @@ extern "C" int pkv_paged_attention_multi_query_quant(
     a.num_blocks = num_blocks;
     a.max_blocks = max_blocks;
     a.max_q_len = max_q_len;
+    a.groups = int4 ? head_dim / group_size : 1;
+    a.int4 = int4;
     a.scale_log2 = scale * pkv::kLog2e;
     a.out = out;
     a.status = st;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (dtype == PKV_DTYPE_BF16) pkv::launch_rows_t<__nv_bfloat16>(a, head_dim, qmode, group_size, cs);
-    else pkv::launch_rows_t<__half>(a, head_dim, qmode, group_size, cs);
-    return pkv::launch_status();
+    const bool bf16 = dtype == PKV_DTYPE_BF16;
+    const int nt = pkv::small_nt(batch, num_kv_heads, max_blocks, static_cast<int64_t>(max_q_len) * a.G);
+    if (nt == 0) return pkv::launch_slice_quant(a, head_dim, bf16, static_cast<float*>(workspace), cs);
+    const int nwt = pkv::small_warps(static_cast<int64_t>(batch) * num_kv_heads * max_blocks, nt);
+    float* ws_o = static_cast<float*>(workspace);
+    float* ws_ml = ws_o + static_cast<size_t>(nwt + static_cast<int64_t>(batch) * num_kv_heads) * 8 * nt * head_dim;
+    return bf16 ? pkv::run_small_t<__nv_bfloat16>(a, head_dim, nt, nwt, ws_o, ws_ml, cs)
+                : pkv::run_small_t<__half>(a, head_dim, nt, nwt, ws_o, ws_ml, cs);
 }
