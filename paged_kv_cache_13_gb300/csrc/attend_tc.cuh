@@ -26,6 +26,8 @@
 // (bounded) for its own copies and MMAs, and the CTA frees its TMEM.
 #pragma once
 
+#include <atomic>
+
 #include "tc5.cuh"
 
 namespace pkv {
@@ -478,6 +480,26 @@ inline int num_splits(int64_t ctas, int64_t tiles, int sms) {
     if (n > tiles / kMinTiles) n = tiles / kMinTiles;
     if (n > kMaxSplits) n = kMaxSplits;
     return n < 1 ? 1 : static_cast<int>(n);
+}
+
+// Sets the kernel's shared memory limit, once per device, and checks that it
+// was built with the registers its warpgroups' split needs (setmaxnreg.inc
+// would otherwise wait for them).
+template <auto kernel>
+int prepare_kernel(int bytes, int regs) {
+    static std::atomic<int> state[64];  // 0: not yet, 1: ready, 2: too few registers
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_ERR_CUDA;
+    int s = state[dev].load(std::memory_order_acquire);
+    if (s == 0) {
+        cudaFuncAttributes fa;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+            cudaFuncGetAttributes(&fa, kernel) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        s = fa.numRegs >= regs ? 1 : 2;
+        state[dev].store(s, std::memory_order_release);
+    }
+    return s == 1 ? PKV_OK : PKV_ERR_UNSUPPORTED;
 }
 
 }  // namespace tcattn

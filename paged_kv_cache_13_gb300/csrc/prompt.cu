@@ -18,7 +18,6 @@
 #include <cuda.h>
 #include <math.h>
 
-#include <atomic>
 #include <mutex>
 
 #include "attend_tc.cuh"
@@ -362,29 +361,9 @@ int prompt_splits(int64_t batch, int64_t T, int64_t S, int64_t hkv, int64_t G) {
     return num_splits(num_slots(batch, T, G) * hkv, (S / batch + kKeys - 1) / kKeys, num_sms());
 }
 
-// Sets the kernel's shared memory limit, once per device, and checks that it
-// was built with the registers its warpgroups' split needs (setmaxnreg.inc
-// would otherwise wait for them).
-template <auto kernel>
-int prepare_kernel(int bytes) {
-    static std::atomic<int> state[64];  // 0: not yet, 1: ready, 2: too few registers
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PKV_ERR_CUDA;
-    int s = state[dev].load(std::memory_order_acquire);
-    if (s == 0) {
-        cudaFuncAttributes fa;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
-            cudaFuncGetAttributes(&fa, kernel) != cudaSuccess)
-            return PKV_ERR_CUDA;
-        s = fa.numRegs >= kLaunchRegs ? 1 : 2;
-        state[dev].store(s, std::memory_order_release);
-    }
-    return s == 1 ? PKV_OK : PKV_ERR_UNSUPPORTED;
-}
-
 template <typename T, int D>
 int launch_prompt(const CUtensorMap& km, const CUtensorMap& vm, const PromptArgs& a, cudaStream_t st) {
-    const int rc = prepare_kernel<prompt_tc_kernel<T, D>>(Layout<D>::kBytes);
+    const int rc = prepare_kernel<prompt_tc_kernel<T, D>>(Layout<D>::kBytes, kLaunchRegs);
     if (rc != PKV_OK) return rc;
     const int64_t slots = num_slots(a.batch, a.T, a.G);
     const unsigned ctas = static_cast<unsigned>(slots * a.hkv);

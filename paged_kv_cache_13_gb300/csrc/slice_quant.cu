@@ -1,117 +1,423 @@
 // Multi-query attention over the quantised cache for more than 24 rows per
 // (sequence, KV head): slices of a prompt, wide verify passes.
-// One warp per (query token, query head) row: the lanes share the head dim,
-// the keys are taken one at a time with an online softmax in fp32.
+//
+// The tensor-core attention of attend_tc.cuh with K/V tiles made by four
+// unpacking warps: they read the codes of a tile's 8 blocks (16 bytes a lane,
+// whole rows), dequantise them to fp16 -- (c - z) and the product with s each
+// rounded to fp16 -- and write them into the ring with the MMAs' swizzle, so a
+// block is unpacked once per 256 query rows.  Sink and window rows are copied
+// as fp16, slots past the context as zeros.  Everything is fp16: queries and
+// values beyond +-65504 saturate (bf16 would cost each value 8 times the
+// rounding error, and K and V are within a factor of 2 of their originals).
+// INT4 codes come out of a word as the pairs (0, 4) (1, 5) (2, 6) (3, 7) of its
+// eight columns and stay in that order: the query takes the same order, the
+// output is put back when it is stored.
+// While an item (K or V of a tile) is unpacked, each 16-byte piece's
+// registers take the next item's load, so codes are in flight all the time.
+// ~2.4 instructions a value, 32,768 values a tile: about a third of the issue
+// slots of a tile's 2,600 cycles.
 
 #include "slice_quant.cuh"
 
-#include "common.cuh"
+#include "attend_tc.cuh"
+#include "balanced.cuh"
 
 namespace pkv {
 namespace {
 
+using namespace tcattn;
+
 constexpr int BS = 16;
+constexpr int kThreads = 512;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8-11: unpacking; 12: MMAs
+constexpr int kWarpUnpack = 8, kWarpMma = 12;
+// Registers: launched at 128 a thread, then softmax 176, unpacking 96, MMAs 64.
+constexpr int kLaunchRegs = 128;
+static_assert(2 * 128 * 176 + 128 * 96 + 128 * 64 <= kThreads * kLaunchRegs, "register split");
 
-// E consecutive values, from column col on, of the K (x = 0) or V (x = 1) row
-// at position t of sequence b; false on a bad table entry.
-template <typename T, int D, int QMODE, int E>
-__device__ __forceinline__ bool row_values(const QuantCache& a, int x, int b, int kvh, int t, int w0, int group, int col,
-                                           float (&v)[E]) {
+template <int D, int QMODE, int NG>
+struct Codes {
+    static constexpr bool INT4 = QMODE == PKV_QMODE_INT4_ASYM;
+    static constexpr int CB = INT4 ? D / 2 : D;  // code bytes per row
+    static constexpr int CPR = CB / 16;          // 16-byte pieces per row
+    static constexpr int RPI = 32 / CPR;         // rows a warp reads per load
+    static constexpr int LPB = BS / RPI;         // loads per block and lane
+    static constexpr int OUT = INT4 ? 4 : 2;     // 16-byte fp16 chunks per piece
+};
+
+__device__ __forceinline__ uint32_t h2(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+
+// fp16 of x, finite values saturating
+__device__ __forceinline__ __half sat16(float x) {
+    return __float2half_rn(fabsf(x) <= 3.4e38f ? fminf(fmaxf(x, -65504.f), 65504.f) : x);
+}
+
+// Eight 16-bit values as fp16 in stored order.
+template <typename T, bool PERM>
+__device__ __forceinline__ uint4 as_fp16(uint4 v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (!std::is_same<T, __half>::value) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const T* e = reinterpret_cast<const T*>(&w[i]);
+            w[i] = h2(__halves2half2(sat16(Half16<T>::to_float(e[0])), sat16(Half16<T>::to_float(e[1]))));
+        }
+    }
+    if constexpr (!PERM) return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(__byte_perm(w[0], w[2], 0x5410u), __byte_perm(w[0], w[2], 0x7632u),
+                      __byte_perm(w[1], w[3], 0x5410u), __byte_perm(w[1], w[3], 0x7632u));
+}
+
+// The sequence a CTA works for.
+struct Seq {
+    int b, kvh, ctx, w0, sinks, nblk;
+};
+
+// The value at (token t, column d) of V, as the kernel reads it (the rare path
+// that puts non-finite values back).
+template <typename T, int D, int QMODE, int NG>
+__device__ float value_at(const QuantCache& a, const Seq& s, int t, int d) {
     const T* src = nullptr;
-    if (t >= w0)
-        src = static_cast<const T*>(a.win[x]) +
-              (((static_cast<int64_t>(b) * a.ring + (t / BS) % a.ring) * a.hkv + kvh) * BS + t % BS) * D;
-    else if (t < a.n_sink)
-        src = static_cast<const T*>(a.sink[x]) + ((static_cast<int64_t>(b) * a.n_sink + t) * a.hkv + kvh) * D;
-    if (src) {
-        for (int e = 0; e < E; ++e) v[e] = Half16<T>::to_float(src[col + e]);
-        return true;
-    }
-    const int phys = a.tables[static_cast<int64_t>(b) * a.max_blocks + t / BS];
-    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.num_blocks)) return false;
-    const int64_t row = (static_cast<int64_t>(phys) * a.hkv + kvh) * BS + t % BS;
-    for (int e = 0; e < E; ++e) {
-        const int d = col + e;
-        if (QMODE == PKV_QMODE_INT4_ASYM) {
-            const int ng = D / group, gi = d / group;
-            const int c = (a.codes[x][row * (D / 2) + d / 2] >> (4 * (d & 1))) & 15;
-            v[e] = (c - __half2float(a.zero[x][row * ng + gi])) * __half2float(a.scale[x][row * ng + gi]);
-        } else {
-            unsigned pair;
-            const unsigned short code = a.codes[x][row * D + d];
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"(code));
-            v[e] = __half2float(__ushort_as_half(static_cast<unsigned short>(pair & 0xffff))) *
-                   __half2float(a.scale[x][row]);
-        }
-    }
-    return true;
+    if (t >= s.w0)
+        src = static_cast<const T*>(a.win[1]) +
+              (((static_cast<int64_t>(s.b) * a.ring + (t / BS) % a.ring) * a.hkv + s.kvh) * BS + t % BS) * D;
+    else if (t < s.sinks)
+        src = static_cast<const T*>(a.sink[1]) + ((static_cast<int64_t>(s.b) * a.n_sink + t) * a.hkv + s.kvh) * D;
+    if (src) return Half16<T>::to_float(src[d]);
+    if (QMODE == PKV_QMODE_INT4_ASYM) return 0.f;  // always finite
+    const int phys = a.tables[static_cast<int64_t>(s.b) * a.max_blocks + t / BS];
+    if (static_cast<unsigned>(phys) >= static_cast<unsigned>(a.num_blocks)) return 0.f;
+    const int64_t row = (static_cast<int64_t>(phys) * a.hkv + s.kvh) * BS + t % BS;
+    return (a.codes[1][row * D + d] & 0x7f) == 0x7f ? __int_as_float(0x7fc00000) : 0.f;
 }
 
-template <typename T, int D, int QMODE>
-__global__ void slice_rows_kernel(const __grid_constant__ QuantCache a, int group) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int h = blockIdx.y, b = blockIdx.z, kvh = h / a.G;
-    const int q0 = a.q_start[b], L = a.q_start[b + 1] - q0;
-    const int cap = a.max_blocks * BS;
-    int ctx = a.ctx_lens[b];
-    if (L <= 0 || i >= min(L, a.max_q_len)) return;
-    if ((ctx < L || ctx > cap || L > a.max_q_len) && lane == 0 && h == 0 && i == 0)
+// The unpacking warps: warp u (0 .. 3) fills rows 32 u .. +31 (blocks 2u, 2u +
+// 1) of every ring item.
+template <typename T, int D, int QMODE, int NG>
+__device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache& a, const Work& w, const Seq& s, int u) {
+    using C = Codes<D, QMODE, NG>;
+    using Y = Layout<D>;
+    constexpr bool PERM = C::INT4;
+    const int lane = threadIdx.x & 31, r = lane % C::RPI, c = lane / C::RPI;
+    const int gi = NG == 2 ? c / (C::CPR / 2) : 0;
+    const int32_t* trow = a.tables + static_cast<int64_t>(s.b) * a.max_blocks;
+    struct Piece {
+        uint4 code;
+        __half scale, zero;
+    };
+    Piece p[2][C::LPB];
+    bool bad = false;
+    // the two blocks' rows of the pool for tile jj (-1: nothing to read there:
+    // past the context, in the window, or a bad table entry)
+    int64_t row0[2];
+    auto find = [&](int jj) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int lb = (w.js + jj) * (kKeys / BS) + 2 * u + x;
+            row0[x] = -1;
+            if (jj < w.n && lb < s.nblk && lb * BS < s.w0) {
+                const int phys = __ldg(trow + lb);
+                if (static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks))
+                    row0[x] = (static_cast<int64_t>(phys) * a.hkv + s.kvh) * BS;
+                else
+                    bad = true;
+            }
+        }
+    };
+    auto load = [&](int x, int i, int kv, const int64_t (&rows)[2]) {
+        if (rows[x] < 0) return;
+        const int64_t row = rows[x] + i * C::RPI + r;
+        p[x][i].code = ldg_stream((kv ? a.codes[1] : a.codes[0]) + row * C::CB + 16 * c);
+        p[x][i].scale = (kv ? a.scale[1] : a.scale[0])[row * NG + gi];
+        if constexpr (C::INT4) p[x][i].zero = (kv ? a.zero[1] : a.zero[0])[row * NG + gi];
+    };
+    find(0);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < C::LPB; ++i) load(x, i, 0, row0);
+    bool odd = false;
+    for (int it = 0; it < 2 * w.n && !sm.stopped(); ++it) {
+        const int jj = it >> 1, kv = it & 1;
+        if (it >= Y::kStages && !__all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFree + sm.slot(it)), sm.phase(it - Y::kStages)))) {
+            if (lane == 0) sm.give_up(a.status);
+            break;
+        }
+        uint8_t* tile = sm.ring(it);
+        const bool guard = kv && w.masked(jj);  // V of a tile some row must not see whole
+        int64_t cur[2] = {row0[0], row0[1]};
+        if (kv) find(jj + 1);  // the next item is K of the next tile
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int t0 = (w.js + jj) * kKeys + (2 * u + x) * BS;
+            // blocks with sinks, window rows or slots past the context
+            const bool special = cur[x] < 0 || t0 + BS > s.ctx || t0 < s.sinks;
+#pragma unroll
+            for (int i = 0; i < C::LPB; ++i) {
+                const int row = i * C::RPI + r, t = t0 + row;
+                uint4 out[C::OUT];
+                const Piece& q = p[x][i];
+                const uint32_t word4[4] = {q.code.x, q.code.y, q.code.z, q.code.w};
+                const __half2 sc = __half2half2(q.scale);
+                if constexpr (C::INT4) {
+                    const __half2 z = __half2half2(q.zero), k1024 = as_h2(0x64006400u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            // 1024 + c, c, c - z, (c - z) s
+                            const __half2 h = as_h2(((word4[j] >> (4 * n)) & 0x000F000Fu) | 0x64006400u);
+                            v[n] = h2(__hmul2(__hsub2(__hsub2(h, k1024), z), sc));
+                        }
+                        out[j] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    const float zf = __half2float(q.zero);
+                    if (fmaxf(fabsf(zf), fabsf(15.f - zf)) * __half2float(q.scale) > 65504.f) {  // may saturate
+                        uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            o[n] = h2(__hmax2(__hmin2(as_h2(o[n]), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            const uint32_t wd = word4[2 * j + n / 2] >> (16 * (n & 1));
+                            uint32_t h;
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(wd & 0xffffu)));
+                            v[n] = h2(__hmul2(as_h2(h), sc));
+                        }
+                        out[j] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    if (__half2float(q.scale) > 65504.f / 448.f) {  // may saturate; NaN codes stay
+                        uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+                        for (int n = 0; n < 8; ++n)
+                            o[n] = h2(__hmax2_nan(__hmin2_nan(as_h2(o[n]), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
+                    }
+                }
+                if (special) {
+                    const T* src = nullptr;
+                    if (t < s.ctx) {
+                        if (t >= s.w0)
+                            src = static_cast<const T*>(kv ? a.win[1] : a.win[0]) +
+                                  (((static_cast<int64_t>(s.b) * a.ring + (t / BS) % a.ring) * a.hkv + s.kvh) * BS + t % BS) * D;
+                        else if (t < s.sinks)
+                            src = static_cast<const T*>(kv ? a.sink[1] : a.sink[0]) +
+                                  ((static_cast<int64_t>(s.b) * a.n_sink + t) * a.hkv + s.kvh) * D;
+                    }
+                    if (src || t >= s.ctx || cur[x] < 0) {
+#pragma unroll
+                        for (int j = 0; j < C::OUT; ++j)
+                            out[j] = src ? as_fp16<T, PERM>(*reinterpret_cast<const uint4*>(src + (C::OUT * c + j) * 8))
+                                         : make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (guard) {  // non-finite values: out, and back in for the rows that see them
+                    uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+                    for (int n = 0; n < 4 * C::OUT; ++n) {
+                        if ((o[n] & 0x7C00u) == 0x7C00u) { o[n] &= 0xffff0000u; odd = true; }
+                        if ((o[n] & 0x7C000000u) == 0x7C000000u) { o[n] &= 0x0000ffffu; odd = true; }
+                    }
+                }
+                const int rr = (2 * u + x) * BS + row;
+#pragma unroll
+                for (int j = 0; j < C::OUT; ++j) *reinterpret_cast<uint4*>(tile + tile_off(rr, C::OUT * c + j)) = out[j];
+                load(x, i, kv ^ 1, row0);
+            }
+        }
+        if (__any_sync(0xffffffffu, odd) && lane == 0) *sm.odd() = 1;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.bar(Y::kFull + sm.slot(it)));
+    }
+    if (bad) atomicOr(a.status, PKV_STATUS_BAD_BLOCK);
+}
+
+template <typename T, int D, int QMODE, int NG>
+__global__ void __launch_bounds__(kThreads, 1)
+    slice_tc_kernel(const __grid_constant__ QuantCache a, int splits, float* ws_o, float* ws_ml) {
+    using Y = Layout<D>;
+    constexpr bool PERM = QMODE == PKV_QMODE_INT4_ASYM;
+    constexpr int kCh = D / 8;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const Smem<D> sm(smem_raw);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    // a sequence's later rows see more keys: they go first
+    const int x = gridDim.x - 1 - blockIdx.x, split = x % splits, tile_row = x / splits;
+    Seq s;
+    s.kvh = blockIdx.y;
+    s.b = blockIdx.z;
+    const int q0 = a.q_start[s.b], L = a.q_start[s.b + 1] - q0, cap = a.max_blocks * BS;
+    const int ctx = a.ctx_lens[s.b];
+    s.ctx = min(max(ctx, 0), cap);
+    s.w0 = a.window > 0 ? max(s.ctx - a.window, 0) / BS * BS : s.ctx;
+    s.sinks = s.w0 > 0 ? a.n_sink : 0;
+    s.nblk = (s.ctx + BS - 1) / BS;
+    Work w;
+    w.row0 = tile_row * kCtaRows;
+    w.G = a.G;
+    w.rows = min(L, a.max_q_len) * a.G;
+    w.first_pos = s.ctx - L;
+    if (L <= 0 || w.row0 >= w.rows) return;
+    if (threadIdx.x == 0 && tile_row == 0 && s.kvh == 0 && split == 0 &&
+        (ctx < L || ctx > cap || L > a.max_q_len))
         atomicOr(a.status, PKV_STATUS_BAD_CONTEXT);
-    ctx = min(max(ctx, 0), cap);
-    const int pos = ctx - L + i;
-    const int w0 = a.window > 0 ? max(ctx - a.window, 0) / BS * BS : ctx;
-    const T* q = static_cast<const T*>(a.q) + ((static_cast<int64_t>(q0) + i) * a.hq + h) * D + lane * E;
-    float x[E], o[E], m = neg_inf(), l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        x[e] = Half16<T>::to_float(q[e]);
-        o[e] = 0.f;
-    }
-    for (int t = 0; t <= pos; ++t) {
-        float v[E];
-        if (!row_values<T, D, QMODE, E>(a, 0, b, kvh, t, w0, group, lane * E, v)) {
-            if (lane == 0) atomicOr(a.status, PKV_STATUS_BAD_BLOCK);
-            continue;
+    w.set_tiles(split, splits);
+    const int tile = warp >> 2;  // 0, 1: softmax
+    const T* qbase = static_cast<const T*>(a.q) + (static_cast<int64_t>(q0) * a.hq + s.kvh * a.G) * D;
+    if (warp == kWarpUnpack && lane == 0) {
+        sm.init(4);
+    } else if (warp == kWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sh_addr(sm.tmem_slot())),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (tile < 2) {
+        // the warp's 32 query rows as fp16, whole 128-byte lines at a time
+        constexpr int kStep = 32 / kCh;
+        const int rr0 = (warp & 3) * 32 + lane / kCh, ch = lane % kCh;
+        int row = w.row0 + tile * kRows + rr0;
+        int tok = row / a.G, h = row - tok * a.G;
+        uint4 v[kCh];
+#pragma unroll
+        for (int y = 0; y < kCh; ++y) {
+            v[y] = make_uint4(0, 0, 0, 0);
+            if (row < w.rows)
+                v[y] = *reinterpret_cast<const uint4*>(qbase + (static_cast<int64_t>(tok) * a.hq + h) * D + ch * 8);
+            row += kStep;
+            h += kStep;
+            while (h >= a.G) {
+                h -= a.G;
+                ++tok;
+            }
         }
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += x[e] * v[e];
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= a.scale_log2;
-        if (s == neg_inf()) continue;
-        const float mn = fmaxf(m, s);
-        const float al = ex2(m - mn), p = ex2(s - mn);
-        m = mn;
-        l = l * al + p;
-        row_values<T, D, QMODE, E>(a, 1, b, kvh, t, w0, group, lane * E, v);
-        for (int e = 0; e < E; ++e) o[e] = o[e] * al + p * v[e];
+#pragma unroll
+        for (int y = 0; y < kCh; ++y)
+            *reinterpret_cast<uint4*>(sm.p + Y::kOffQ + tile * Y::kTile + tile_off(rr0 + y * kStep, ch)) =
+                as_fp16<T, PERM>(v[y]);
+        fence_async_shared();
     }
-    T* out = static_cast<T*>(a.out) + ((static_cast<int64_t>(q0) + i) * a.hq + h) * D + lane * E;
-    for (int e = 0; e < E; ++e) out[e] = Half16<T>::from_float(l > 0.f || l != l ? o[e] / l : 0.f);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *sm.tmem_slot();
+
+    if (tile == 2) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        unpack_warp<T, D, QMODE, NG>(sm, a, w, s, warp - kWarpUnpack);
+    } else if (tile == 3) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kWarpMma) mma_warp<__half>(sm, tmem, w, a.status);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        float m, l;
+        const bool ok = softmax_tile<__half>(sm, tmem, w, tile, a.scale_log2, a.status, m, l, [](int) { return true; });
+        const int row = w.row0 + tile * kRows + (warp & 3) * 32 + lane;
+        const int tok = row / a.G, h = row - tok * a.G;
+        const bool odd = w.count(tile) > 0 && *sm.odd() != 0;
+        const int my_pos = w.first_pos + min(row, w.rows - 1) / a.G;
+        auto put_back = [&](int d0, float (&o)[32]) {
+            if (!odd) return;
+            for (int t = w.masked_from(); t <= my_pos && t < min((w.js + w.n) * kKeys, s.ctx); ++t) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float f = value_at<T, D, QMODE, NG>(a, s, t, d0 + (i & ~7) + (i & 7));
+                    if (!(fabsf(f) <= 3.4e38f)) o[(i & ~7) + stored<PERM>(i & 7)] += f;
+                }
+            }
+        };
+        if (splits == 1) {
+            store_tile<T, D, PERM>(sm, tmem, w, tile, l, ok,
+                                   static_cast<T*>(a.out) + (static_cast<int64_t>(q0) * a.hq + s.kvh * a.G) * D, a.hq,
+                                   put_back);
+        } else {
+            const int64_t prow = ((static_cast<int64_t>(split) * a.batch + s.b) * a.max_q_len + tok) * a.hq + s.kvh * a.G + h;
+            store_partial<D, PERM>(tmem, w, tile, m, l, ok && row < w.rows, ws_o, ws_ml, prow, put_back);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
 }
 
-template <typename T, int D, int QMODE>
-void launch_rows(const QuantCache& a, int group, cudaStream_t st) {
-    slice_rows_kernel<T, D, QMODE><<<dim3((a.max_q_len + 3) / 4, a.hq, a.batch), 128, 0, st>>>(a, group);
+// Merge of the splits: one CTA per 256 rows, a warp per row at a time.
+constexpr int kMergeWarps = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    slice_merge_kernel(const __grid_constant__ QuantCache a, int splits, const float* ws_o, const float* ws_ml) {
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    const int q0 = a.q_start[b], L = a.q_start[b + 1] - q0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (L <= 0) return;
+    const int rows = min(L, a.max_q_len) * a.G, end = min((static_cast<int>(blockIdx.x) + 1) * kCtaRows, rows);
+    for (int row = blockIdx.x * kCtaRows + (threadIdx.x >> 5); row < end; row += kMergeWarps) {
+        const int tok = row / a.G, h = kvh * a.G + row - tok * a.G;
+        merge_row<T, D>(ws_o, ws_ml, splits, static_cast<int64_t>(a.batch) * a.max_q_len * a.hq,
+                        (static_cast<int64_t>(b) * a.max_q_len + tok) * a.hq + h,
+                        static_cast<T*>(a.out) + ((static_cast<int64_t>(q0) + tok) * a.hq + h) * D);
+    }
+}
+
+int64_t row_tiles(int64_t max_q_len, int64_t G) { return (max_q_len * G + kCtaRows - 1) / kCtaRows; }
+
+int slice_splits(int64_t batch, int64_t hkv, int64_t G, int64_t max_blocks, int64_t max_q_len) {
+    return num_splits(row_tiles(max_q_len, G) * hkv * batch, (max_blocks * BS + kKeys - 1) / kKeys, num_sms());
+}
+
+template <typename T, int D, int QMODE, int NG>
+int launch(const QuantCache& a, float* workspace, cudaStream_t st) {
+    const int rc = prepare_kernel<slice_tc_kernel<T, D, QMODE, NG>>(Layout<D>::kBytes, kLaunchRegs);
+    if (rc != PKV_OK) return rc;
+    const int splits = slice_splits(a.batch, a.hkv, a.G, a.max_blocks, a.max_q_len);
+    const unsigned tiles = static_cast<unsigned>(row_tiles(a.max_q_len, a.G));
+    float* ws_ml = splits > 1 ? workspace + static_cast<size_t>(splits) * a.batch * a.max_q_len * a.hq * D : nullptr;
+    slice_tc_kernel<T, D, QMODE, NG>
+        <<<dim3(tiles * splits, a.hkv, a.batch), kThreads, Layout<D>::kBytes, st>>>(a, splits, workspace, ws_ml);
+    if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    if (splits == 1) return PKV_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles, a.hkv, a.batch);
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, slice_merge_kernel<T, D>, a, splits, static_cast<const float*>(workspace),
+                              static_cast<const float*>(ws_ml)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
 }
 
 template <typename T>
-void launch_rows_t(const QuantCache& a, int D, cudaStream_t st) {
-    const int group = D / a.groups;
-    if (D == 128 && a.int4) launch_rows<T, 128, PKV_QMODE_INT4_ASYM>(a, group, st);
-    else if (D == 128) launch_rows<T, 128, PKV_QMODE_FP8_E4M3>(a, group, st);
-    else if (a.int4) launch_rows<T, 64, PKV_QMODE_INT4_ASYM>(a, group, st);
-    else launch_rows<T, 64, PKV_QMODE_FP8_E4M3>(a, group, st);
+int launch_t(const QuantCache& a, int D, float* ws, cudaStream_t st) {
+    if (a.int4) {
+        if (D == 64) return launch<T, 64, PKV_QMODE_INT4_ASYM, 1>(a, ws, st);
+        return a.groups == 2 ? launch<T, 128, PKV_QMODE_INT4_ASYM, 2>(a, ws, st)
+                             : launch<T, 128, PKV_QMODE_INT4_ASYM, 1>(a, ws, st);
+    }
+    return D == 64 ? launch<T, 64, PKV_QMODE_FP8_E4M3, 1>(a, ws, st) : launch<T, 128, PKV_QMODE_FP8_E4M3, 1>(a, ws, st);
 }
 
 }  // namespace
 
-size_t slice_quant_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t slice_quant_workspace(int64_t batch, int64_t hq, int64_t hkv, int64_t D, int64_t max_blocks, int64_t max_q_len) {
+    const int n = slice_splits(batch, hkv, hq / hkv, max_blocks, max_q_len);
+    return n == 1 ? 0 : static_cast<size_t>(n) * batch * max_q_len * hq * (D + 2) * sizeof(float);
+}
 
-int launch_slice_quant(const QuantCache& a, int D, bool bf16, float*, cudaStream_t st) {
-    if (bf16) launch_rows_t<__nv_bfloat16>(a, D, st);
-    else launch_rows_t<__half>(a, D, st);
-    return launch_status();
+int launch_slice_quant(const QuantCache& a, int D, bool bf16, float* workspace, cudaStream_t st) {
+    return bf16 ? launch_t<__nv_bfloat16>(a, D, workspace, st) : launch_t<__half>(a, D, workspace, st);
 }
 
 }  // namespace pkv
