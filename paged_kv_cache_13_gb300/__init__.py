@@ -146,10 +146,21 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_current_raw_stream = None
+
+
 def _stream(stream):
+    global _current_raw_stream
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_raw_stream is None:
+            # the raw handle alone where torch offers it: building a Stream
+            # object costs 3 us a call
+            torch.cuda.current_stream()  # initialises CUDA
+            raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            _current_raw_stream = (lambda: raw(dev())) if raw and dev else (
+                lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -429,11 +440,12 @@ def pkv_paged_attention_multi_query(q, q_start, k_pool, v_pool, block_tables, co
 def _row_stride(t, name):
     """Elements between the rows of t [T, H, D], whose rows are dense."""
     T, H, D = t.shape
+    row, head, dim = t.stride()
     if T == 0:
         return H * D
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    if (dim != 1 and D > 1) or (head != D and H > 1):
         raise ValueError("%s: heads and dims must be contiguous within a row, got strides %s" % (name, t.stride()))
-    return t.stride(0) if T > 1 else max(t.stride(0), H * D)
+    return row if T > 1 else max(row, H * D)
 
 
 def pkv_prompt_attention_workspace_bytes(batch, num_tokens, num_kv_tokens, num_q_heads, num_kv_heads, head_dim):
@@ -583,13 +595,14 @@ def pkv_move_rows(pools, src_slots, dst_slots, stream=None):
         raise ValueError("src_slots and dst_slots have one length")
     if n == 0:
         return
-    NB, Hkv, BS = pools[0].shape[:3]
+    NB, Hkv, BS = shape = pools[0].shape[:3]
+    k = len(pools)
     for p in pools:
-        if tuple(p.shape[:3]) != (NB, Hkv, BS) or not p.is_contiguous():
+        if p.shape[:3] != shape or not p.is_contiguous():
             raise ValueError("pools are dense [num_blocks, num_kv_heads, block_size, ...] of one shape")
-    ptrs = (_vp * len(pools))(*[p.data_ptr() for p in pools])
-    bpr = (_i64 * len(pools))(*[p[0, 0, 0].numel() * p.element_size() for p in pools])
-    _check(lib.pkv_move_rows(ptrs, bpr, len(pools), _ptr(src_slots), _ptr(dst_slots), n, NB, Hkv, BS,
+    ptrs = (_vp * k)(*[p.data_ptr() for p in pools])
+    bpr = (_i64 * k)(*[p.stride(2) * p.element_size() for p in pools])
+    _check(lib.pkv_move_rows(ptrs, bpr, k, _ptr(src_slots), _ptr(dst_slots), n, NB, Hkv, BS,
                              _stream(stream)), "pkv_move_rows")
 
 

@@ -18,10 +18,14 @@
 // as N) see exact codes, the scales and zero points factored out:
 //   QK^T: S_t = s_t (sum_d q_d c_td - z_t sum_d q_d)
 //   PV:   O_d = sum_t W_t c_td - sum_t W_t z_t,  W_t = P_t s_t (fp16)
-// INT4 codes are used as fp16 subnormals (a nibble masked in place: c 2^-24,
-// the next nibble 16 c 2^-24; the query columns and outputs that meet the
-// latter are scaled to match), FP8 codes convert exactly.  sum_t W_t z_t is one
-// more MMA per n-tile: the zero points as a 17th row of V.
+// INT4 codes of K are used as fp16 subnormals (a nibble masked in place: c
+// 2^-24, the next nibble 16 c 2^-24; the query columns that meet the latter are
+// divided by 16), those of V as c - 8 (the nibble put under 1024's mantissa,
+// 1032 taken off; 16 (c - 8) for the next nibble, undone at the end): sums over
+// a long context of codes that are all positive, less the zero points', would
+// lose ten bits to cancellation (16k tokens: 1.5e-3 relative).  FP8 codes
+// convert exactly.  sum_t W_t (z_t - 8) is one more MMA per n-tile: the zero
+// points as a 17th row of V.
 // Sinks and window blocks are 16-bit blocks attended after the quantised ones
 // of a run, with the accumulator taken to true units first.
 //
@@ -55,6 +59,10 @@ constexpr int kMinItems = 8;
 __device__ __forceinline__ uint32_t nib_even(uint32_t w) { return w & 0x000F000Fu; }
 __device__ __forceinline__ uint32_t nib_odd(uint32_t w) { return w & 0x00F000F0u; }
 __device__ __forceinline__ uint32_t f16pair(float lo, float hi) { return Half16<__half>::pack(lo, hi); }
+__device__ __forceinline__ uint32_t sub16x2(uint32_t a, uint32_t b) {
+    const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     Half16<__half>::mma(d, a0, a1, a2, a3, b0, b1);
@@ -166,7 +174,9 @@ struct VCodes {
             const int word = e >> 3, sub = (e >> 2) & 1, nib = e & 3;
             const uint32_t x = __byte_perm(a[word], b[word], sub ? 0x7632u : 0x5410u);
             const uint32_t y = nib >= 2 ? x >> 8 : x;
-            return (nib & 1) ? nib_odd(y) : nib_even(y);
+            // c - 8, or 16 (c - 8): exact in fp16
+            const uint32_t h = ((nib & 1) ? nib_odd(y) : nib_even(y)) | 0x64006400u;
+            return sub16x2(h, (nib & 1) ? 0x64806480u : 0x64086408u);
         } else {
             const int word = e >> 2, sub = e & 3;
             const uint32_t x = __byte_perm(a[word], b[word], (sub >> 1) ? 0x7362u : 0x5140u);
@@ -203,6 +213,11 @@ struct Scales {
                 vz[NG - 1][0] = __byte_perm(x.x, x.y, 0x7632u);
                 vz[0][1] = __byte_perm(y.x, y.y, 0x5410u);
                 vz[NG - 1][1] = __byte_perm(y.x, y.y, 0x7632u);
+            }
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {  // z - 8, as V's codes are taken
+                vz[i][0] = sub16x2(vz[i][0], 0x48004800u);
+                vz[i][1] = sub16x2(vz[i][1], 0x48004800u);
             }
         }
     }
@@ -580,8 +595,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             phys = pn;
         }
 
-        // ---- to true units: INT4 products are in 2^-24 (odd nibbles 2^-20),
-        // and the zero points come off
+        // ---- INT4: the odd nibbles' 16 and the zero points come off
         if constexpr (S::INT4) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -592,7 +606,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
                 for (int mt = 0; mt < MT; ++mt) {
                     const int el = pv_e<D, NG>(mt, 0);
                     const int gi = (el >> 3) / S::VPG;
-                    const float u = (el & 1) ? kTwo24 * 0.0625f : kTwo24;
+                    const float u = (el & 1) ? 0.0625f : 1.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) w.o[mt][nt][j] = fmaf(w.o[mt][nt][j], u, -cr[2 * gi + (j & 1)]);
                 }
