@@ -29,18 +29,23 @@
 // Sinks and window blocks are 16-bit blocks attended after the quantised ones
 // of a run, with the accumulator taken to true units first.
 //
+// A block's K and V codes, scales and zero points are 6 contiguous runs (4 for
+// FP8): lanes 0 .. 5 copy one each into the warp's ring of kStages blocks in
+// shared memory (untiled asynchronous copies, one mbarrier a stage), kStages
+// blocks ahead; 16-bit blocks go through the same ring, two at a time.
 // Bound: HBM in bytes (1,088 per token and layer for 8 heads of INT4), in
-// practice the issue slots: ~290 instructions per block and KV head at 24
-// rows.  The next block's codes are loaded as soon as their registers are
-// free (K after QK^T, V after PV).
+// practice the issue slots of the 8 warps an SM's registers hold at 24 rows.
 
 #include <math.h>
 
 #include "balanced.cuh"
 #include "slice_quant.cuh"
+#include "tc5.cuh"
 
 namespace pkv {
 namespace {
+
+using namespace tc5;
 
 constexpr int BS = 16;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -50,8 +55,10 @@ constexpr float kNoMax = -1e30f;        // reference maximum of a row that has s
 constexpr float kTwo24 = 16777216.f;    // 2^24
 constexpr int kWarps = 2;               // warps per CTA
 constexpr int kMaxNT = 3;               // n-tiles of 8 rows per warp, at most
-// resident CTAs per SM, as the registers of NT n-tiles allow
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 6 : 4; }
+constexpr int kStages = 4;              // quantised blocks in a warp's ring
+// resident CTAs per SM, as the registers of NT n-tiles (and, for one, the
+// rings) allow
+constexpr int ctas_per_sm(int nt) { return nt == 3 ? 4 : 5; }
 // Fewest items a warp takes: short runs cost a partial row set each, which
 // the merge reads back.
 constexpr int kMinItems = 8;
@@ -81,7 +88,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "r"(addr));
     return r;
 }
-__device__ __forceinline__ float half_at(const __half* p) { return __half2float(*p); }
 template <typename T>
 constexpr bool kSplitP = false;
 template <>
@@ -109,34 +115,40 @@ struct Shape {
     static constexpr int KW = INT4 ? D / 32 : D / 16;  // 32-bit K-code words per lane and row
     static constexpr int VW = INT4 ? D / 64 : D / 32;  // 32-bit V-code words per lane and row
     static constexpr int KPG = KW / NG, VPG = VW / NG;
+    // a block of one KV head in the ring: K codes, V codes, then the scales of
+    // K and V and the zero points of K and V
+    static constexpr int CODES = BS * CB, SCALES = BS * NG * 2;
+    static constexpr int COPIES = INT4 ? 6 : 4;
+    static constexpr int STAGE = 2 * CODES + (COPIES - 2) * SCALES;
+    static constexpr int STAGE16 = 2 * BS * D * 2;  // a 16-bit block: K rows, V rows
     static_assert(NG == 1 || (INT4 && D == 128 && NG == 2), "groups: one per head, or 64 columns at D 128");
 };
 
-// One block's codes of a lane: K rows g, g + 8; V rows 2c, 2c + 1, 8 + 2c, 9 +
-// 2c.  kp / vp point at the lane's first bytes of the block's rows.
+// One block's codes of a lane, from the ring: K rows g, g + 8; V rows 2c, 2c +
+// 1, 8 + 2c, 9 + 2c.  p points at the lane's first bytes of the first row.
 template <int D, int QMODE, int NG>
 struct KCodes {
     using S = Shape<D, QMODE, NG>;
     uint32_t r0[S::KW], r1[S::KW];
-    __device__ __forceinline__ void load(const uint8_t* kp) {
+    __device__ __forceinline__ void load(const uint8_t* p) {
         if constexpr (!S::INT4) {
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) put<4>(4 * i, kp + 64 * i);
+            for (int i = 0; i < D / 64; ++i) put<4>(4 * i, p + 64 * i);
         } else if constexpr (NG == 2) {
-            put<2>(0, kp);
-            put<2>(2, kp + 32);
+            put<2>(0, p);
+            put<2>(2, p + 32);
         } else {
-            put<S::KW>(0, kp);
+            put<S::KW>(0, p);
         }
     }
     template <int N>
     __device__ __forceinline__ void put(int at, const uint8_t* p) {
         if constexpr (N == 4) {
-            const uint4 x = ldg_stream(p), y = ldg_stream(p + 8 * S::CB);
+            const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8 * S::CB);
             r0[at] = x.x; r0[at + 1] = x.y; r0[at + 2] = x.z; r0[at + 3] = x.w;
             r1[at] = y.x; r1[at + 1] = y.y; r1[at + 2] = y.z; r1[at + 3] = y.w;
         } else {
-            const uint2 x = ldg_stream8(p), y = ldg_stream8(p + 8 * S::CB);
+            const uint2 x = *reinterpret_cast<const uint2*>(p), y = *reinterpret_cast<const uint2*>(p + 8 * S::CB);
             r0[at] = x.x; r0[at + 1] = x.y;
             r1[at] = y.x; r1[at + 1] = y.y;
         }
@@ -147,21 +159,21 @@ template <int D, int QMODE, int NG>
 struct VCodes {
     using S = Shape<D, QMODE, NG>;
     uint32_t r[4][S::VW];
-    __device__ __forceinline__ void load(const uint8_t* vp) {
-        row(0, vp);
-        row(1, vp + S::CB);
-        row(2, vp + 8 * S::CB);
-        row(3, vp + 9 * S::CB);
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        row(0, p);
+        row(1, p + S::CB);
+        row(2, p + 8 * S::CB);
+        row(3, p + 9 * S::CB);
     }
     __device__ __forceinline__ void row(int i, const uint8_t* p) {
         if constexpr (NG == 2) {
             r[i][0] = *reinterpret_cast<const uint32_t*>(p);
             r[i][1] = *reinterpret_cast<const uint32_t*>(p + 32);
         } else if constexpr (S::VW == 4) {
-            const uint4 x = ldg_stream(p);
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
             r[i][0] = x.x; r[i][1] = x.y; r[i][2] = x.z; r[i][3] = x.w;
         } else if constexpr (S::VW == 2) {
-            const uint2 x = ldg_stream8(p);
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
             r[i][0] = x.x; r[i][1] = x.y;
         } else {
             r[i][0] = *reinterpret_cast<const uint32_t*>(p);
@@ -191,17 +203,17 @@ template <int D, int QMODE, int NG>
 struct Scales {
     __half2 ks[NG], vs[NG], kz[NG];  // low: token g, high: token g + 8
     uint32_t vz[NG][2];
-    __device__ __forceinline__ void load(const QuantCache& a, int64_t row0, int g, int c) {
-        const int64_t s0 = (row0 + g) * NG;
-        const __half *k = a.scale[0] + s0, *v = a.scale[1] + s0;
+    __device__ __forceinline__ void load(const uint8_t* p, int g, int c) {  // p: the stage's scales
+        const __half* k = reinterpret_cast<const __half*>(p) + g * NG;
+        const __half* v = k + BS * NG;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             ks[i] = __halves2half2(k[i], k[8 * NG + i]);
             vs[i] = __halves2half2(v[i], v[8 * NG + i]);
         }
         if constexpr (Shape<D, QMODE, NG>::INT4) {
-            const __half* kzp = a.zero[0] + s0;
-            const __half* z = a.zero[1] + (row0 + 2 * c) * NG;
+            const __half* kzp = k + 2 * BS * NG;
+            const __half* z = reinterpret_cast<const __half*>(p) + 3 * BS * NG + 2 * c * NG;
 #pragma unroll
             for (int i = 0; i < NG; ++i) kz[i] = __halves2half2(kzp[i], kzp[8 * NG + i]);
             if constexpr (NG == 1) {
@@ -223,38 +235,38 @@ struct Scales {
     }
 };
 
-// A warp's state over its run: lane (g, c) holds rows 8 nt + 2c, 8 nt + 2c + 1
-// of every n-tile.  corr: the zero-point MMA's accumulator (rows 0 and 8 of its
-// 16: column groups 0 and 1; lanes g = 0).
+// A warp's state over its run: lane (g, c) holds rows 8 nt + 2c (x), 8 nt + 2c +
+// 1 (y) of every n-tile.  nm: minus the reference maximum.  corr: the
+// zero-point MMA's accumulator (rows 0 and 8 of its 16: column groups 0 and 1;
+// lanes g = 0).
 template <int MT, int NT>
 struct State {
-    float m[NT][2], l[NT][2];
+    float2 nm[NT], l[NT];
     float o[MT][NT][4];
     float corr[NT][4];
 };
 
-// Raises the reference maxima to cover the logits x (of all n-tiles) and
-// rescales what was accumulated against the old ones.
+// Raises n-tile nt's reference maxima to cover the logits x (tokens g: 0, 1;
+// tokens g + 8: 2, 3) and rescales what was accumulated against the old ones.
 template <int MT, int NT>
-__device__ __forceinline__ void raise_max(State<MT, NT>& w, const float (&x)[NT][4]) {
+__device__ __forceinline__ void raise_max(State<MT, NT>& w, int nt, const float (&x)[4]) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int k = 0; k < 2; ++k) {
+        float b = fmaxf(x[k], x[k + 2]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float b = fmaxf(x[nt][k], x[nt][k + 2]);
+        for (int off = 4; off < 32; off <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
+        float& nm = k ? w.nm[nt].y : w.nm[nt].x;
+        float& l = k ? w.l[nt].y : w.l[nt].x;
+        const float mn = fmaxf(-nm, b);
+        const float al = ex2(-nm - mn);
+        nm = -mn;
+        l *= al;
+        w.corr[nt][k] *= al;
+        w.corr[nt][k + 2] *= al;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
-            const float mn = fmaxf(w.m[nt][k], b);
-            const float al = ex2(w.m[nt][k] - mn);
-            w.m[nt][k] = mn;
-            w.l[nt][k] *= al;
-            w.corr[nt][k] *= al;
-            w.corr[nt][k + 2] *= al;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                w.o[mt][nt][k] *= al;
-                w.o[mt][nt][k + 2] *= al;
-            }
+        for (int mt = 0; mt < MT; ++mt) {
+            w.o[mt][nt][k] *= al;
+            w.o[mt][nt][k + 2] *= al;
         }
     }
 }
@@ -289,12 +301,30 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;");
-    // per warp: the run's query fragments ([NT][QW][32] uint4) while it
-    // attends, then its R x D partial outputs
-    static_assert(R * D >= NT * QW * 32 * 4, "slice too small for the query fragments");
-    __shared__ __align__(16) float slice[kWarps][R * D];
-    uint4* sq = reinterpret_cast<uint4*>(&slice[warp][0]) + lane;
-    const uint32_t qs_addr = static_cast<uint32_t>(__cvta_generic_to_shared(sq));
+    // per warp: the run's query fragments ([NT][QW][32] uint4) and the ring,
+    // which takes the run's R x D partial outputs when the run is done
+    constexpr int kMax = S::STAGE * kStages > 2 * S::STAGE16 ? S::STAGE * kStages : 2 * S::STAGE16;
+    constexpr int kRing = kMax > R * D * 4 ? kMax : R * D * 4;
+    static_assert(kStages == 4 && kRing % 16 == 0, "ring");
+    __shared__ __align__(128) uint8_t rings[kWarps][kRing];
+    __shared__ __align__(16) uint4 queries[kWarps][NT * QW * 32];
+    __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+    uint8_t* ring = rings[warp];
+    const uint32_t ring_addr = sh_addr(ring), bar0 = sh_addr(bars[warp]);
+    uint4* sq = queries[warp] + lane;
+    const uint32_t qs_addr = sh_addr(sq);
+    if (lane < kStages) mbar_init(bar0 + 8 * lane, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_shared();
+    __syncwarp();
+    uint32_t par = 0;  // parity of each stage's next fill
+    // waits for stage s; false (and the status bit) when its copies never land
+    auto landed = [&](int s) {
+        const bool ok = __all_sync(0xffffffffu, wait_bar(bar0 + 8 * s, (par >> s) & 1u));
+        par ^= 1u << s;
+        if (!ok && lane == 0) atomicOr(a.status, PKV_STATUS_COPY_TIMEOUT);
+        return ok;
+    };
 
     const int i = blockIdx.x * kWarps + warp;
     const int cap = a.max_blocks * BS;
@@ -384,8 +414,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
         State<MT, NT> w;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            w.m[nt][0] = w.m[nt][1] = kNoMax;
-            w.l[nt][0] = w.l[nt][1] = 0.f;
+            w.nm[nt] = make_float2(-kNoMax, -kNoMax);
+            w.l[nt] = make_float2(0.f, 0.f);
             w.corr[nt][0] = w.corr[nt][1] = w.corr[nt][2] = w.corr[nt][3] = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) w.o[mt][nt][0] = w.o[mt][nt][1] = w.o[mt][nt][2] = w.o[mt][nt][3] = 0.f;
@@ -398,43 +428,55 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
         // exist aside: their outputs go nowhere)
         const int full_lb = max(first_pos + 1, 0) / BS;
 
-        // ---- quantised blocks
-        const uint8_t* kbase = a.codes[0] + g * S::CB +
-                               (!S::INT4 ? 16 * c : NG == 2 ? 8 * c : (KW == 4 ? 16 * c : 8 * c));
-        const uint8_t* vbase = a.codes[1] + 2 * c * S::CB + (S::INT4 ? (NG == 2 ? 4 * g : D / 16 * g) : D / 8 * g);
+        // ---- quantised blocks.  Lane j copies run j of a block (see Shape):
+        // from src + phys * step into the stage at dst.
+        const bool scales = lane >= 2;
+        const uint8_t* src = lane == 0   ? a.codes[0]
+                             : lane == 1 ? a.codes[1]
+                                         : reinterpret_cast<const uint8_t*>(lane < 4 ? a.scale[lane & 1] : a.zero[lane & 1]);
+        const uint32_t bytes = scales ? S::SCALES : S::CODES, step = bytes * a.hkv;
+        const uint32_t dst = ring_addr + (scales ? 2 * S::CODES + (lane - 2) * S::SCALES : lane * S::CODES);
+        src += static_cast<uint32_t>(kvh) * bytes;
         const int32_t* trow = a.tables + static_cast<int64_t>(b) * a.max_blocks;
-        auto row0_of = [&](int phys) { return (static_cast<int64_t>(phys) * a.hkv + kvh) * BS; };
-        auto valid = [&](int phys) { return static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks); };
-        int tab = sp.lb0 + lane < q_end ? trow[sp.lb0 + lane] : -1;
-        int phys = __shfl_sync(0xffffffffu, tab, 0);
-        KCodes<D, QMODE, NG> kc;
-        VCodes<D, QMODE, NG> vc;
-        Scales<D, QMODE, NG> sc;
-        if (sp.lb0 < q_end && valid(phys)) {
-            kc.load(kbase + row0_of(phys) * S::CB);
-            vc.load(vbase + row0_of(phys) * S::CB);
-            sc.load(a, row0_of(phys), g, c);
-        }
-        for (int lb = sp.lb0, k = 0; lb < q_end; ++lb, ++k) {
-            int pn = -1;
-            if (lb + 1 < q_end) {
-                if (((k + 1) & 31) == 0) {  // ids of the run's next 32 blocks
-                    const int idx = lb + 1 + lane;
-                    tab = idx < q_end ? trow[idx] : -1;
-                }
-                pn = __shfl_sync(0xffffffffu, tab, (k + 1) & 31);
+        const int nq = q_end - sp.lb0;
+        int tab = -1;
+        uint32_t filled = 0;  // stages with a block to attend
+        auto issue = [&](int k) {  // block lb0 + k into stage k % kStages
+            if ((k & 31) == 0) {
+                tab = k + lane < nq ? trow[sp.lb0 + k + lane] : -1;
+                if (__any_sync(0xffffffffu, k + lane < nq && static_cast<unsigned>(tab) >= static_cast<unsigned>(a.num_blocks)) &&
+                    lane == 0)
+                    atomicOr(a.status, PKV_STATUS_BAD_BLOCK);
             }
-            const bool nv = valid(pn);
-            if (!valid(phys)) {
-                if (lane == 0) atomicOr(a.status, PKV_STATUS_BAD_BLOCK);
-                if (nv) {  // nothing attended: fetch the next block now
-                    kc.load(kbase + row0_of(pn) * S::CB);
-                    vc.load(vbase + row0_of(pn) * S::CB);
-                    sc.load(a, row0_of(pn), g, c);
-                }
-                phys = pn;
+            const int phys = __shfl_sync(0xffffffffu, tab, k & 31);
+            const int s = k % kStages;
+            filled &= ~(1u << s);
+            if (static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks)) {
+                filled |= 1u << s;
+                if (lane == 0) mbar_arrive_expect_tx(bar0 + 8 * s, S::STAGE);
+                __syncwarp();
+                if (lane < S::COPIES)
+                    bulk_load(dst + s * S::STAGE, src + static_cast<uint64_t>(static_cast<uint32_t>(phys)) * step, bytes,
+                              bar0 + 8 * s);
+            }
+        };
+        for (int k = 0; k < min(nq, kStages); ++k) issue(k);
+        for (int k = 0; k < nq; ++k) {
+            const int lb = sp.lb0 + k;
+            const uint8_t* stage = ring + (k % kStages) * S::STAGE;
+            if (!((filled >> (k % kStages)) & 1u)) {  // a bad table entry: nothing to attend
+                if (k + kStages < nq) issue(k + kStages);
                 continue;
             }
+            if (!landed(k % kStages)) {  // the copies still in flight land (bounded), then the warp stops
+                for (int j = k + 1; j < min(nq, k + kStages); ++j)
+                    if ((filled >> (j % kStages)) & 1u) landed(j % kStages);
+                return;
+            }
+            KCodes<D, QMODE, NG> kc;
+            kc.load(stage + g * S::CB + (!S::INT4 ? 16 * c : NG == 2 ? 8 * c : (KW == 4 ? 16 * c : 8 * c)));
+            Scales<D, QMODE, NG> sc;
+            sc.load(stage + 2 * S::CODES, g, c);
             // ---- S^T = C Q^T over the code values, per column group
             float s[NG][NT][4];
 #pragma unroll
@@ -462,48 +504,52 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
                     mma_f16(s[gi][nt], f[4], f[5], f[6], f[7], q.z, q.w);
                 }
             }
-            if (nv) kc.load(kbase + row0_of(pn) * S::CB);
-
-            // ---- logits (base 2)
-            float x[NT][4];
+            // ---- logits (base 2) less the reference maxima; k0, z0: token g's
+            // scale and -scale * zero point, k1, z1: token g + 8's
+            float k0[NG], k1[NG], z0[NG], z1[NG], vs0[NG], vs1[NG];
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-                const float k0 = __low2float(sc.ks[gi]) * a.scale_log2, k1 = __high2float(sc.ks[gi]) * a.scale_log2;
-                float z0 = 0.f, z1 = 0.f;
+                k0[gi] = __low2float(sc.ks[gi]) * a.scale_log2;
+                k1[gi] = __high2float(sc.ks[gi]) * a.scale_log2;
                 if constexpr (S::INT4) {
-                    z0 = -k0 * __low2float(sc.kz[gi]);
-                    z1 = -k1 * __high2float(sc.kz[gi]);
+                    z0[gi] = -k0[gi] * __low2float(sc.kz[gi]);
+                    z1[gi] = -k1[gi] * __high2float(sc.kz[gi]);
+                    k0[gi] *= kTwo24;
+                    k1[gi] *= kTwo24;
                 }
-                const float m0 = S::INT4 ? k0 * kTwo24 : k0, m1 = S::INT4 ? k1 * kTwo24 : k1;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float sv = s[gi][nt][j], mul = j < 2 ? m0 : m1;
-                        float y = gi == 0 ? sv * mul : fmaf(sv, mul, x[nt][j]);
-                        if constexpr (S::INT4) y = fmaf(j < 2 ? z0 : z1, qs[nt][gi][j & 1], y);
-                        x[nt][j] = y;
-                    }
-                }
-            }
-            const int t0 = lb * BS;
-            const bool masked = lb >= full_lb || (lb == 0 && sinks > 0);
-            bool fix_nan = false;
-            float vs0[NG], vs1[NG];
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
                 vs0[gi] = __low2float(sc.vs[gi]);
                 vs1[gi] = __high2float(sc.vs[gi]);
             }
+            // from: what is added to the scaled products
+            auto logits = [&](int nt, float2 from, float2& e0, float2& e1) {
+                e0 = e1 = from;
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    if constexpr (S::INT4) {
+                        const float2 q = make_float2(qs[nt][gi][0], qs[nt][gi][1]);
+                        e0 = fma2(make_float2(z0[gi], z0[gi]), q, e0);
+                        e1 = fma2(make_float2(z1[gi], z1[gi]), q, e1);
+                    }
+                    e0 = fma2(make_float2(s[gi][nt][0], s[gi][nt][1]), make_float2(k0[gi], k0[gi]), e0);
+                    e1 = fma2(make_float2(s[gi][nt][2], s[gi][nt][3]), make_float2(k1[gi], k1[gi]), e1);
+                }
+            };
+            float2 d0[NT], d1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) logits(nt, w.nm[nt], d0[nt], d1[nt]);
+            VCodes<D, QMODE, NG> vc;
+            vc.load(stage + S::CODES + 2 * c * S::CB + (S::INT4 ? (NG == 2 ? 4 * g : D / 16 * g) : D / 8 * g));
+            const int t0 = lb * BS;
+            const bool masked = lb >= full_lb || (lb == 0 && sinks > 0);
+            bool fix_nan = false;
             if (masked) {
                 const bool in0 = t0 + g < ctx && t0 + g >= sinks, in1 = t0 + g + 8 < ctx && t0 + g + 8 >= sinks;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int k2 = 0; k2 < 2; ++k2) {
-                        if (!in0 || t0 + g > pos[nt][k2]) x[nt][k2] = neg_inf();
-                        if (!in1 || t0 + g + 8 > pos[nt][k2]) x[nt][k2 + 2] = neg_inf();
-                    }
+                    if (!in0 || t0 + g > pos[nt][0]) d0[nt].x = neg_inf();
+                    if (!in0 || t0 + g > pos[nt][1]) d0[nt].y = neg_inf();
+                    if (!in1 || t0 + g + 8 > pos[nt][0]) d1[nt].x = neg_inf();
+                    if (!in1 || t0 + g + 8 > pos[nt][1]) d1[nt].y = neg_inf();
                 }
                 // slots that hold no token, and sinks: any bits; their weight is
                 // 0, their scale and zero point are taken out
@@ -539,27 +585,34 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             }
 
             // ---- online softmax: the reference maxima move only when a logit
-            // exceeds them by more than kSlack, or a V scale is large
-            bool up = false;
+            // exceeds one by more than kSlack, or a V scale is large
+            float top = neg_inf(), vtop = 0.f;
 #pragma unroll
-            for (int gi = 0; gi < NG; ++gi) up |= fmaxf(vs0[gi], vs1[gi]) > kLazyMaxScale;
+            for (int nt = 0; nt < NT; ++nt) top = max3f(top, fmaxf(d0[nt].x, d0[nt].y), fmaxf(d1[nt].x, d1[nt].y));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                up |= fmaxf(x[nt][0], x[nt][2]) > w.m[nt][0] + kSlack;
-                up |= fmaxf(x[nt][1], x[nt][3]) > w.m[nt][1] + kSlack;
+            for (int gi = 0; gi < NG; ++gi) vtop = max3f(vtop, vs0[gi], vs1[gi]);
+            if (__any_sync(0xffffffffu, top > kSlack || vtop > kLazyMaxScale)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float2 x0, x1;
+                    logits(nt, make_float2(0.f, 0.f), x0, x1);
+                    const float x[4] = {d0[nt].x == neg_inf() ? neg_inf() : x0.x, d0[nt].y == neg_inf() ? neg_inf() : x0.y,
+                                        d1[nt].x == neg_inf() ? neg_inf() : x1.x, d1[nt].y == neg_inf() ? neg_inf() : x1.y};
+                    raise_max<MT, NT>(w, nt, x);
+                    d0[nt] = add2(make_float2(x[0], x[1]), w.nm[nt]);
+                    d1[nt] = add2(make_float2(x[2], x[3]), w.nm[nt]);
+                }
             }
-            if (__any_sync(0xffffffffu, up)) raise_max<MT, NT>(w, x);
             uint32_t b0[NG][NT], b1[NG][NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = ex2(x[nt][0] - w.m[nt][0]), p1 = ex2(x[nt][1] - w.m[nt][1]);
-                const float p2 = ex2(x[nt][2] - w.m[nt][0]), p3 = ex2(x[nt][3] - w.m[nt][1]);
-                w.l[nt][0] += p0 + p2;
-                w.l[nt][1] += p1 + p3;
+                const float2 p0 = make_float2(ex2(d0[nt].x), ex2(d0[nt].y)), p1 = make_float2(ex2(d1[nt].x), ex2(d1[nt].y));
+                w.l[nt] = add2(w.l[nt], add2(p0, p1));
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
-                    b0[gi][nt] = movmatrix_trans(f16pair(p0 * vs0[gi], p1 * vs0[gi]));
-                    b1[gi][nt] = movmatrix_trans(f16pair(p2 * vs1[gi], p3 * vs1[gi]));
+                    const float2 w0 = mul2(p0, make_float2(vs0[gi], vs0[gi])), w1 = mul2(p1, make_float2(vs1[gi], vs1[gi]));
+                    b0[gi][nt] = movmatrix_trans(f16pair(w0.x, w0.y));
+                    b1[gi][nt] = movmatrix_trans(f16pair(w1.x, w1.y));
                 }
             }
             // ---- sum_t W_t z_t: zero points as row 0 (group 0) and 8 (group 1)
@@ -573,7 +626,6 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
                                 b1[NG - 1][nt]);
                 }
             }
-            if (nv) sc.load(a, row0_of(pn), g, c);
             // ---- O^T += C_v^T W^T
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -585,14 +637,14 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             }
             if constexpr (!S::INT4) {
                 if (fix_nan) {
-                    const uint8_t* codes = a.codes[1] + row0_of(phys) * S::CB;
+                    const uint8_t* codes = stage + S::CODES;
                     add_non_finite<D, NG, NT>(w, pos, max(t0, sinks), min(t0 + BS, ctx), g, [&](int t, int col) {
                         return (codes[(t - t0) * S::CB + col] & 0x7f) == 0x7f ? __int_as_float(0x7fc00000) : 0.f;
                     });
                 }
             }
-            if (nv) vc.load(vbase + row0_of(pn) * S::CB);
-            phys = pn;
+            __syncwarp();  // the stage is read
+            if (k + kStages < nq) issue(k + kStages);
         }
 
         // ---- INT4: the odd nibbles' 16 and the zero points come off
@@ -614,18 +666,40 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
         }
 
         // ---- 16-bit blocks: the sinks (their rows stand in for block 0's first
-        // n_sink tokens), then the window.  kr / vr: row 0, rows apart by
-        // `stride`; tokens t0 .. t0 + n - 1.
-        auto attend16 = [&](const T* kr, const T* vr, int64_t stride, int t0, int n) {
+        // n_sink tokens), then the window, through the ring two at a time: lane
+        // r < 16 copies K row r, lane 16 + r V row r.
+        constexpr int kRow16 = D * 2;
+        const int win0 = max(sp.lb0, win_lb), n_win = max(sp.lb1 - win0, 0);
+        const int sink_rows = sp.lb0 == 0 ? min(sinks, ctx) : 0;
+        const int n16 = (sink_rows > 0 ? 1 : 0) + n_win;
+        auto rows16 = [&](int k, int& t0, int& n) {  // the k-th 16-bit block's first token and rows
+            const int lb = win0 + k - (sink_rows > 0 ? 1 : 0);
+            t0 = sink_rows > 0 && k == 0 ? 0 : lb * BS;
+            n = sink_rows > 0 && k == 0 ? sink_rows : min(BS, ctx - lb * BS);
+        };
+        auto issue16 = [&](int k) {
+            int t0, n;
+            rows16(k, t0, n);
+            const int x = lane >> 4, r = lane & 15, s = k & 1;
+            const T* p = sink_rows > 0 && k == 0
+                             ? static_cast<const T*>(a.sink[x]) +
+                                   ((static_cast<int64_t>(b) * a.n_sink + r) * a.hkv + kvh) * D
+                             : static_cast<const T*>(a.win[x]) +
+                                   (((static_cast<int64_t>(b) * a.ring + (t0 / BS) % a.ring) * a.hkv + kvh) * BS + r) * D;
+            if (lane == 0) mbar_arrive_expect_tx(bar0 + 8 * s, 2 * n * kRow16);
+            __syncwarp();
+            if (r < n) bulk_load(ring_addr + s * S::STAGE16 + (x * BS + r) * kRow16, p, kRow16, bar0 + 8 * s);
+        };
+        auto attend16 = [&](const T* kr, const T* vr, int t0, int n) {
             using H = Half16<T>;
             constexpr int KC = D / 32, VC = D / 64;
-            auto at = [&](int r) { return min(r, n - 1) * stride; };  // never past the last row
             float x[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
             for (int k = 0; k < KC; ++k) {
-                const uint4 k0 = ldg_stream(kr + at(g) + 32 * k + 8 * c), k1 = ldg_stream(kr + at(g + 8) + 32 * k + 8 * c);
+                const uint4 k0 = *reinterpret_cast<const uint4*>(kr + g * D + 32 * k + 8 * c);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(kr + (g + 8) * D + 32 * k + 8 * c);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int row = 8 * nt + g;
@@ -642,19 +716,22 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int r = g + 8 * (j >> 1);
+                    const int r = g + 8 * (j >> 1);  // rows past n: whatever the ring held
                     x[nt][j] = r < n && t0 + r <= pos[nt][j & 1] ? x[nt][j] * a.scale_log2 : neg_inf();
-                    up |= x[nt][j] > w.m[nt][j & 1] + kSlack;
+                    up |= x[nt][j] + (j & 1 ? w.nm[nt].y : w.nm[nt].x) > kSlack;
                 }
             }
-            if (__any_sync(0xffffffffu, up)) raise_max<MT, NT>(w, x);
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) raise_max<MT, NT>(w, nt, x[nt]);
+            }
             uint32_t b0[NT], b1[NT], e0[NT], e1[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = ex2(x[nt][0] - w.m[nt][0]), p1 = ex2(x[nt][1] - w.m[nt][1]);
-                const float p2 = ex2(x[nt][2] - w.m[nt][0]), p3 = ex2(x[nt][3] - w.m[nt][1]);
-                w.l[nt][0] += p0 + p2;
-                w.l[nt][1] += p1 + p3;
+                const float p0 = ex2(x[nt][0] + w.nm[nt].x), p1 = ex2(x[nt][1] + w.nm[nt].y);
+                const float p2 = ex2(x[nt][2] + w.nm[nt].x), p3 = ex2(x[nt][3] + w.nm[nt].y);
+                w.l[nt].x += p0 + p2;
+                w.l[nt].y += p1 + p3;
                 const uint32_t h01 = H::pack(p0, p1), h23 = H::pack(p2, p3);
                 b0[nt] = movmatrix_trans(h01);
                 b1[nt] = movmatrix_trans(h23);
@@ -669,16 +746,17 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             for (int j = 0; j < 4; ++j) {
                 const int r = 2 * c + (j & 1) + 8 * (j >> 1);
 #pragma unroll
-                for (int x2 = 0; x2 < VC; ++x2) {
-                    v[j][x2] = r < n ? ldg_stream(vr + at(r) + (NG == 2 ? 64 * x2 + 8 * g : g * (D / 8) + 8 * x2))
-                                     : make_uint4(0, 0, 0, 0);
+                for (int y = 0; y < VC; ++y) {
+                    v[j][y] = make_uint4(0, 0, 0, 0);
+                    if (r < n)
+                        v[j][y] = *reinterpret_cast<const uint4*>(vr + r * D + (NG == 2 ? 64 * y + 8 * g : g * (D / 8) + 8 * y));
                     // non-finite values: out of the product (see add_non_finite)
                     constexpr uint32_t kExp = kSplitP<T> ? 0x7F80u : 0x7C00u;
-                    uint32_t* wd = reinterpret_cast<uint32_t*>(&v[j][x2]);
+                    uint32_t* wd = reinterpret_cast<uint32_t*>(&v[j][y]);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        if ((wd[y] & kExp) == kExp) { wd[y] &= 0xffff0000u; odd = true; }
-                        if (((wd[y] >> 16) & kExp) == kExp) { wd[y] &= 0x0000ffffu; odd = true; }
+                    for (int z = 0; z < 4; ++z) {
+                        if ((wd[z] & kExp) == kExp) { wd[z] &= 0xffff0000u; odd = true; }
+                        if (((wd[z] >> 16) & kExp) == kExp) { wd[z] &= 0x0000ffffu; odd = true; }
                     }
                 }
             }
@@ -699,36 +777,36 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
                 }
             }
             if (__any_sync(0xffffffffu, odd))
-                add_non_finite<D, NG, NT>(w, pos, t0, t0 + n, g, [&](int t, int col) {
-                    const float x2 = Half16<T>::to_float(vr[(t - t0) * stride + col]);
-                    return x2;
-                });
+                add_non_finite<D, NG, NT>(w, pos, t0, t0 + n, g,
+                                          [&](int t, int col) { return Half16<T>::to_float(vr[(t - t0) * D + col]); });
         };
-        if (sp.lb0 == 0 && sinks > 0) {
-            const int64_t at = (static_cast<int64_t>(b) * a.n_sink * a.hkv + kvh) * D;
-            const int n = min(sinks, ctx);
-            if (n > 0)
-                attend16(static_cast<const T*>(a.sink[0]) + at, static_cast<const T*>(a.sink[1]) + at,
-                         static_cast<int64_t>(a.hkv) * D, 0, n);
-        }
-        for (int lb = max(sp.lb0, win_lb); lb < sp.lb1; ++lb) {
-            const int64_t at = ((static_cast<int64_t>(b) * a.ring + lb % a.ring) * a.hkv + kvh) * (BS * D);
-            attend16(static_cast<const T*>(a.win[0]) + at, static_cast<const T*>(a.win[1]) + at, D, lb * BS,
-                     min(BS, ctx - lb * BS));
+        __syncwarp();  // the quantised stages are read
+        for (int k = 0; k < min(n16, 2); ++k) issue16(k);
+        for (int k = 0; k < n16; ++k) {
+            if (!landed(k & 1)) {
+                if (k + 1 < n16) landed((k + 1) & 1);
+                return;
+            }
+            int t0, n;
+            rows16(k, t0, n);
+            const T* kr = reinterpret_cast<const T*>(ring + (k & 1) * S::STAGE16);
+            attend16(kr, kr + BS * D, t0, n);
+            __syncwarp();  // the stage is read
+            if (k + 2 < n16) issue16(k + 2);
         }
 
         // ---- the run's partial rows: l totalled over the token lanes, o
-        // staged through the slice so rows go out in 16-byte stores
+        // staged through the ring so rows go out in 16-byte stores
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
-                w.l[nt][0] += __shfl_xor_sync(0xffffffffu, w.l[nt][0], off);
-                w.l[nt][1] += __shfl_xor_sync(0xffffffffu, w.l[nt][1], off);
+                w.l[nt].x += __shfl_xor_sync(0xffffffffu, w.l[nt].x, off);
+                w.l[nt].y += __shfl_xor_sync(0xffffffffu, w.l[nt].y, off);
             }
         }
-        __syncwarp();  // the query fragments are no longer read
-        float* so = &slice[warp][0];
+        __syncwarp();  // the ring is no longer read
+        float* so = reinterpret_cast<float*>(ring);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -743,6 +821,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
         float4* po = reinterpret_cast<float4*>(ws_o + slot * R * D);
         const float4* s4 = reinterpret_cast<const float4*>(so);
         for (int y = lane; y < rows * D / 4; y += 32) po[y] = s4[y];
+        fence_async_shared();  // before the next run's copies into the ring
         if (g == 0) {
             float* pml = ws_ml + slot * R * 2;
 #pragma unroll
@@ -750,7 +829,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int row = 8 * nt + 2 * c + k;
-                    if (row < rows) *reinterpret_cast<float2*>(pml + 2 * row) = make_float2(w.m[nt][k], w.l[nt][k]);
+                    if (row < rows)
+                        *reinterpret_cast<float2*>(pml + 2 * row) =
+                            k ? make_float2(-w.nm[nt].y, w.l[nt].y) : make_float2(-w.nm[nt].x, w.l[nt].x);
                 }
             }
         }
