@@ -47,6 +47,23 @@ struct Codes {
 __device__ __forceinline__ uint32_t h2(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
+// two e4m3 codes in the low 16 bits of w -> fp16 pair
+__device__ __forceinline__ __half2 e4m3x2(uint32_t w) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<unsigned short>(w & 0xffffu)));
+    return as_h2(d);
+}
+
+// Whether every value of a (scale, zero point) pair is finite and comes out of
+// the short way as of the long one: 0 <= s < 128, and z 0 or 2^-5 <= |z| <=
+// 496, so that s 2^9 is finite, (15 + |z|) s <= 65504, and c - z, a multiple of
+// 2^-15, stays exact at 2^-9 of its size even as a subnormal.
+template <bool INT4>
+__device__ __forceinline__ bool ordinary(__half scale, __half zero) {
+    const unsigned z = __half_as_ushort(zero) & 0x7fffu;
+    return __half_as_ushort(scale) < 0x5800u && (!INT4 || z == 0 || z - 0x2800u <= 0x5FC0u - 0x2800u);
+}
+
 // fp16 of x, finite values saturating
 __device__ __forceinline__ __half sat16(float x) {
     return __float2half_rn(fabsf(x) <= 3.4e38f ? fminf(fmaxf(x, -65504.f), 65504.f) : x);
@@ -137,7 +154,7 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
 #pragma unroll
         for (int i = 0; i < C::LPB; ++i) load(x, i, 0, row0);
     bool odd = false;
-    for (int it = 0; it < 2 * w.n && !sm.stopped(); ++it) {
+    for (int it = 0; it < 2 * w.n && !__any_sync(0xffffffffu, sm.stopped()); ++it) {
         const int jj = it >> 1, kv = it & 1;
         if (it >= Y::kStages && !__all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFree + sm.slot(it)), sm.phase(it - Y::kStages)))) {
             if (lane == 0) sm.give_up(a.status);
@@ -147,6 +164,60 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
         const bool guard = kv && w.masked(jj);  // V of a tile some row must not see whole
         int64_t cur[2] = {row0[0], row0[1]};
         if (kv) find(jj + 1);  // the next item is K of the next tile
+        // ordinary items (all of the warp's blocks quantised and whole, scales
+        // and zero points in range) go straight through, no branch between the
+        // pieces
+        bool plain = true;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int t0 = (w.js + jj) * kKeys + (2 * u + x) * BS;
+            plain &= cur[x] >= 0 && t0 + BS <= s.ctx && t0 >= s.sinks;
+#pragma unroll
+            for (int i = 0; i < C::LPB; ++i) plain &= ordinary<C::INT4>(p[x][i].scale, p[x][i].zero);
+        }
+        if (!C::INT4 && guard) plain = false;  // (INT4: finite)
+        if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int i = 0; i < C::LPB; ++i) {
+                    const Piece& q = p[x][i];
+                    const uint32_t word4[4] = {q.code.x, q.code.y, q.code.z, q.code.w};
+                    const int rr = (2 * u + x) * BS + i * C::RPI + r;
+                    uint4 out[C::OUT];
+                    if constexpr (C::INT4) {
+                        // a nibble masked in place is the subnormal c 2^-24 or 16 c
+                        // 2^-24: (c - z) 2^-9 in one FMA
+                        const __half2 even = as_h2(0x78007800u), odd4 = as_h2(0x68006800u);  // 2^15, 2^11
+                        const __half2 mz = __half2half2(__hmul(q.zero, __ushort_as_half(0x9800)));    // -z 2^-9
+                        const __half2 sc = __half2half2(__hmul(q.scale, __ushort_as_half(0x6000)));   // s 2^9
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo = word4[j], hi = lo >> 8;
+                            out[j].x = h2(__hmul2(__hfma2(as_h2(lo & 0x000F000Fu), even, mz), sc));
+                            out[j].y = h2(__hmul2(__hfma2(as_h2(lo & 0x00F000F0u), odd4, mz), sc));
+                            out[j].z = h2(__hmul2(__hfma2(as_h2(hi & 0x000F000Fu), even, mz), sc));
+                            out[j].w = h2(__hmul2(__hfma2(as_h2(hi & 0x00F000F0u), odd4, mz), sc));
+                        }
+                    } else {
+                        const __half2 sc = __half2half2(q.scale);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            out[j] = make_uint4(h2(__hmul2(e4m3x2(word4[2 * j]), sc)), h2(__hmul2(e4m3x2(word4[2 * j] >> 16), sc)),
+                                                h2(__hmul2(e4m3x2(word4[2 * j + 1]), sc)),
+                                                h2(__hmul2(e4m3x2(word4[2 * j + 1] >> 16), sc)));
+                    }
+#pragma unroll
+                    for (int j = 0; j < C::OUT; ++j)
+                        *reinterpret_cast<uint4*>(tile + tile_off(rr, C::OUT * c + j)) = out[j];
+                    load(x, i, kv ^ 1, row0);
+                }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sm.bar(Y::kFull + sm.slot(it)));
+            continue;
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int t0 = (w.js + jj) * kKeys + (2 * u + x) * BS;
@@ -185,10 +256,7 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
                         uint32_t v[4];
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            const uint32_t wd = word4[2 * j + n / 2] >> (16 * (n & 1));
-                            uint32_t h;
-                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(wd & 0xffffu)));
-                            v[n] = h2(__hmul2(as_h2(h), sc));
+                            v[n] = h2(__hmul2(e4m3x2(word4[2 * j + n / 2] >> (16 * (n & 1))), sc));
                         }
                         out[j] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
