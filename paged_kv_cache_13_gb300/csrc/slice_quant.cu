@@ -124,18 +124,28 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
     };
     Piece p[2][C::LPB];
     bool bad = false;
-    // the two blocks' rows of the pool for tile jj (-1: nothing to read there:
-    // past the context, in the window, or a bad table entry)
+    // the two blocks of tile jj: their table entries (fetched a tile ahead of
+    // their use: the codes' addresses wait for them) and their rows of the pool
+    // (-1: nothing to read there: past the context, in the window, or a bad
+    // entry)
+    int phys[2];
     int64_t row0[2];
+    auto quantised = [&](int jj, int x) {
+        const int lb = (w.js + jj) * (kKeys / BS) + 2 * u + x;
+        return jj < w.n && lb < s.nblk && lb * BS < s.w0;
+    };
+    auto fetch = [&](int jj) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (quantised(jj, x)) phys[x] = __ldg(trow + (w.js + jj) * (kKeys / BS) + 2 * u + x);
+    };
     auto find = [&](int jj) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int lb = (w.js + jj) * (kKeys / BS) + 2 * u + x;
             row0[x] = -1;
-            if (jj < w.n && lb < s.nblk && lb * BS < s.w0) {
-                const int phys = __ldg(trow + lb);
-                if (static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks))
-                    row0[x] = (static_cast<int64_t>(phys) * a.hkv + s.kvh) * BS;
+            if (quantised(jj, x)) {
+                if (static_cast<unsigned>(phys[x]) < static_cast<unsigned>(a.num_blocks))
+                    row0[x] = (static_cast<int64_t>(phys[x]) * a.hkv + s.kvh) * BS;
                 else
                     bad = true;
             }
@@ -148,7 +158,9 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
         p[x][i].scale = (kv ? a.scale[1] : a.scale[0])[row * NG + gi];
         if constexpr (C::INT4) p[x][i].zero = (kv ? a.zero[1] : a.zero[0])[row * NG + gi];
     };
+    fetch(0);
     find(0);
+    fetch(1);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -163,7 +175,10 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
         uint8_t* tile = sm.ring(it);
         const bool guard = kv && w.masked(jj);  // V of a tile some row must not see whole
         int64_t cur[2] = {row0[0], row0[1]};
-        if (kv) find(jj + 1);  // the next item is K of the next tile
+        if (kv) {  // the next item is K of the next tile
+            find(jj + 1);
+            fetch(jj + 2);
+        }
         // ordinary items (all of the warp's blocks quantised and whole, scales
         // and zero points in range) go straight through, no branch between the
         // pieces
