@@ -28,11 +28,12 @@ namespace {
 using namespace tcattn;
 
 constexpr int BS = 16;
-constexpr int kThreads = 512;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8-11: unpacking; 12: MMAs
-constexpr int kWarpUnpack = 8, kWarpMma = 12;
-// Registers: launched at 128 a thread, then softmax 176, unpacking 96, MMAs 64.
+constexpr int kThreads = 512;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8-14: unpacking; 15: MMAs
+constexpr int kWarpUnpack = 8, kUnpackWarps = 7, kWarpMma = 15;
+constexpr int kBlocks = kKeys / BS;  // blocks of a ring item
+// Registers: launched at 128 a thread, then softmax 176, the others 80.
 constexpr int kLaunchRegs = 128;
-static_assert(2 * 128 * 176 + 128 * 96 + 128 * 64 <= kThreads * kLaunchRegs, "register split");
+static_assert(2 * 128 * 176 + 2 * 128 * 80 <= kThreads * kLaunchRegs, "register split");
 
 template <int D, int QMODE, int NG>
 struct Codes {
@@ -108,8 +109,10 @@ __device__ float value_at(const QuantCache& a, const Seq& s, int t, int d) {
     return (a.codes[1][row * D + d] & 0x7f) == 0x7f ? __int_as_float(0x7fc00000) : 0.f;
 }
 
-// The unpacking warps: warp u (0 .. 3) fills rows 32 u .. +31 (blocks 2u, 2u +
-// 1) of every ring item.
+// The unpacking warps: block x of ring item it is job 8 it + x, and warp u takes
+// jobs u, u + 7, ..: each at its own pace, a job's codes loaded while the one
+// before is unpacked and its table entry a job earlier still (the codes'
+// addresses wait for it).
 template <typename T, int D, int QMODE, int NG>
 __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache& a, const Work& w, const Seq& s, int u) {
     using C = Codes<D, QMODE, NG>;
@@ -118,200 +121,171 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
     const int lane = threadIdx.x & 31, r = lane % C::RPI, c = lane / C::RPI;
     const int gi = NG == 2 ? c / (C::CPR / 2) : 0;
     const int32_t* trow = a.tables + static_cast<int64_t>(s.b) * a.max_blocks;
+    const int jobs = 2 * w.n * kBlocks;
     struct Piece {
         uint4 code;
         __half scale, zero;
     };
-    Piece p[2][C::LPB];
+    Piece p[C::LPB];
     bool bad = false;
-    // the two blocks of tile jj: their table entries (fetched a tile ahead of
-    // their use: the codes' addresses wait for them) and their rows of the pool
-    // (-1: nothing to read there: past the context, in the window, or a bad
-    // entry)
-    int phys[2];
-    int64_t row0[2];
-    auto quantised = [&](int jj, int x) {
-        const int lb = (w.js + jj) * (kKeys / BS) + 2 * u + x;
-        return jj < w.n && lb < s.nblk && lb * BS < s.w0;
+    // a job's block of the sequence; its table entry (-1: nothing to read
+    // there: past the context, or in the window)
+    auto block = [&](int job) { return (w.js + job / (2 * kBlocks)) * kBlocks + job % kBlocks; };
+    auto fetch = [&](int job) {
+        const int lb = block(job);
+        return job < jobs && lb < s.nblk && lb * BS < s.w0 ? __ldg(trow + lb) : -1;
     };
-    auto fetch = [&](int jj) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            if (quantised(jj, x)) phys[x] = __ldg(trow + (w.js + jj) * (kKeys / BS) + 2 * u + x);
+    auto find = [&](int job, int phys) -> int64_t {  // the block's first row in the pool, or -1
+        if (static_cast<unsigned>(phys) < static_cast<unsigned>(a.num_blocks))
+            return (static_cast<int64_t>(phys) * a.hkv + s.kvh) * BS;
+        const int lb = block(job);
+        if (job < jobs && lb < s.nblk && lb * BS < s.w0) bad = true;
+        return -1;
     };
-    auto find = [&](int jj) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            row0[x] = -1;
-            if (quantised(jj, x)) {
-                if (static_cast<unsigned>(phys[x]) < static_cast<unsigned>(a.num_blocks))
-                    row0[x] = (static_cast<int64_t>(phys[x]) * a.hkv + s.kvh) * BS;
-                else
-                    bad = true;
-            }
-        }
+    auto load = [&](int i, int kv, int64_t row0) {
+        if (row0 < 0) return;
+        const int64_t row = row0 + i * C::RPI + r;
+        p[i].code = ldg_stream((kv ? a.codes[1] : a.codes[0]) + row * C::CB + 16 * c);
+        p[i].scale = (kv ? a.scale[1] : a.scale[0])[row * NG + gi];
+        if constexpr (C::INT4) p[i].zero = (kv ? a.zero[1] : a.zero[0])[row * NG + gi];
     };
-    auto load = [&](int x, int i, int kv, const int64_t (&rows)[2]) {
-        if (rows[x] < 0) return;
-        const int64_t row = rows[x] + i * C::RPI + r;
-        p[x][i].code = ldg_stream((kv ? a.codes[1] : a.codes[0]) + row * C::CB + 16 * c);
-        p[x][i].scale = (kv ? a.scale[1] : a.scale[0])[row * NG + gi];
-        if constexpr (C::INT4) p[x][i].zero = (kv ? a.zero[1] : a.zero[0])[row * NG + gi];
-    };
-    fetch(0);
-    find(0);
-    fetch(1);
+    int64_t next = find(u, fetch(u));
+    int phys = fetch(u + kUnpackWarps);
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < C::LPB; ++i) load(x, i, 0, row0);
+    for (int i = 0; i < C::LPB; ++i) load(i, 0, next);
     bool odd = false;
-    for (int it = 0; it < 2 * w.n && !__any_sync(0xffffffffu, sm.stopped()); ++it) {
-        const int jj = it >> 1, kv = it & 1;
+    for (int job = u; job < jobs && !__any_sync(0xffffffffu, sm.stopped()); job += kUnpackWarps) {
+        const int it = job / kBlocks, jj = it >> 1, kv = it & 1;
         if (it >= Y::kStages && !__all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFree + sm.slot(it)), sm.phase(it - Y::kStages)))) {
             if (lane == 0) sm.give_up(a.status);
             break;
         }
         uint8_t* tile = sm.ring(it);
         const bool guard = kv && w.masked(jj);  // V of a tile some row must not see whole
-        int64_t cur[2] = {row0[0], row0[1]};
-        if (kv) {  // the next item is K of the next tile
-            find(jj + 1);
-            fetch(jj + 2);
-        }
-        // ordinary items (all of the warp's blocks quantised and whole, scales
-        // and zero points in range) go straight through, no branch between the
-        // pieces
-        bool plain = true;
+        const int64_t cur = next;
+        const int t0 = block(job) * BS, row_in = job % kBlocks * BS;
+        const int kv_next = (job + kUnpackWarps) / kBlocks & 1;
+        next = find(job + kUnpackWarps, phys);
+        phys = fetch(job + 2 * kUnpackWarps);
+        // ordinary blocks (quantised and whole, scales and zero points in range)
+        // go straight through, no branch between the pieces
+        bool plain = cur >= 0 && t0 + BS <= s.ctx && t0 >= s.sinks && (C::INT4 || !guard);  // (INT4: finite)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int t0 = (w.js + jj) * kKeys + (2 * u + x) * BS;
-            plain &= cur[x] >= 0 && t0 + BS <= s.ctx && t0 >= s.sinks;
-#pragma unroll
-            for (int i = 0; i < C::LPB; ++i) plain &= ordinary<C::INT4>(p[x][i].scale, p[x][i].zero);
-        }
-        if (!C::INT4 && guard) plain = false;  // (INT4: finite)
+        for (int i = 0; i < C::LPB; ++i) plain &= ordinary<C::INT4>(p[i].scale, p[i].zero);
         if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int i = 0; i < C::LPB; ++i) {
+                const Piece& q = p[i];
+                const uint32_t word4[4] = {q.code.x, q.code.y, q.code.z, q.code.w};
+                const int rr = row_in + i * C::RPI + r;
+                uint4 out[C::OUT];
+                if constexpr (C::INT4) {
+                    // a nibble masked in place is the subnormal c 2^-24 or 16 c
+                    // 2^-24: (c - z) 2^-9 in one FMA
+                    const __half2 even = as_h2(0x78007800u), odd4 = as_h2(0x68006800u);  // 2^15, 2^11
+                    const __half2 mz = __half2half2(__hmul(q.zero, __ushort_as_half(0x9800)));    // -z 2^-9
+                    const __half2 sc = __half2half2(__hmul(q.scale, __ushort_as_half(0x6000)));   // s 2^9
 #pragma unroll
-                for (int i = 0; i < C::LPB; ++i) {
-                    const Piece& q = p[x][i];
-                    const uint32_t word4[4] = {q.code.x, q.code.y, q.code.z, q.code.w};
-                    const int rr = (2 * u + x) * BS + i * C::RPI + r;
-                    uint4 out[C::OUT];
-                    if constexpr (C::INT4) {
-                        // a nibble masked in place is the subnormal c 2^-24 or 16 c
-                        // 2^-24: (c - z) 2^-9 in one FMA
-                        const __half2 even = as_h2(0x78007800u), odd4 = as_h2(0x68006800u);  // 2^15, 2^11
-                        const __half2 mz = __half2half2(__hmul(q.zero, __ushort_as_half(0x9800)));    // -z 2^-9
-                        const __half2 sc = __half2half2(__hmul(q.scale, __ushort_as_half(0x6000)));   // s 2^9
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = word4[j], hi = lo >> 8;
-                            out[j].x = h2(__hmul2(__hfma2(as_h2(lo & 0x000F000Fu), even, mz), sc));
-                            out[j].y = h2(__hmul2(__hfma2(as_h2(lo & 0x00F000F0u), odd4, mz), sc));
-                            out[j].z = h2(__hmul2(__hfma2(as_h2(hi & 0x000F000Fu), even, mz), sc));
-                            out[j].w = h2(__hmul2(__hfma2(as_h2(hi & 0x00F000F0u), odd4, mz), sc));
-                        }
-                    } else {
-                        const __half2 sc = __half2half2(q.scale);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            out[j] = make_uint4(h2(__hmul2(e4m3x2(word4[2 * j]), sc)), h2(__hmul2(e4m3x2(word4[2 * j] >> 16), sc)),
-                                                h2(__hmul2(e4m3x2(word4[2 * j + 1]), sc)),
-                                                h2(__hmul2(e4m3x2(word4[2 * j + 1] >> 16), sc)));
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = word4[j], hi = lo >> 8;
+                        out[j].x = h2(__hmul2(__hfma2(as_h2(lo & 0x000F000Fu), even, mz), sc));
+                        out[j].y = h2(__hmul2(__hfma2(as_h2(lo & 0x00F000F0u), odd4, mz), sc));
+                        out[j].z = h2(__hmul2(__hfma2(as_h2(hi & 0x000F000Fu), even, mz), sc));
+                        out[j].w = h2(__hmul2(__hfma2(as_h2(hi & 0x00F000F0u), odd4, mz), sc));
                     }
+                } else {
+                    const __half2 sc = __half2half2(q.scale);
 #pragma unroll
-                    for (int j = 0; j < C::OUT; ++j)
-                        *reinterpret_cast<uint4*>(tile + tile_off(rr, C::OUT * c + j)) = out[j];
-                    load(x, i, kv ^ 1, row0);
+                    for (int j = 0; j < 2; ++j)
+                        out[j] = make_uint4(h2(__hmul2(e4m3x2(word4[2 * j]), sc)), h2(__hmul2(e4m3x2(word4[2 * j] >> 16), sc)),
+                                            h2(__hmul2(e4m3x2(word4[2 * j + 1]), sc)),
+                                            h2(__hmul2(e4m3x2(word4[2 * j + 1] >> 16), sc)));
                 }
+#pragma unroll
+                for (int j = 0; j < C::OUT; ++j)
+                    *reinterpret_cast<uint4*>(tile + tile_off(rr, C::OUT * c + j)) = out[j];
+                load(i, kv_next, next);
             }
             fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(sm.bar(Y::kFull + sm.slot(it)));
             continue;
         }
+        // blocks with sinks, window rows or slots past the context
+        const bool special = cur < 0 || t0 + BS > s.ctx || t0 < s.sinks;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int t0 = (w.js + jj) * kKeys + (2 * u + x) * BS;
-            // blocks with sinks, window rows or slots past the context
-            const bool special = cur[x] < 0 || t0 + BS > s.ctx || t0 < s.sinks;
+        for (int i = 0; i < C::LPB; ++i) {
+            const int row = i * C::RPI + r, t = t0 + row;
+            uint4 out[C::OUT];
+            const Piece& q = p[i];
+            const uint32_t word4[4] = {q.code.x, q.code.y, q.code.z, q.code.w};
+            const __half2 sc = __half2half2(q.scale);
+            if constexpr (C::INT4) {
+                const __half2 z = __half2half2(q.zero), k1024 = as_h2(0x64006400u);
 #pragma unroll
-            for (int i = 0; i < C::LPB; ++i) {
-                const int row = i * C::RPI + r, t = t0 + row;
-                uint4 out[C::OUT];
-                const Piece& q = p[x][i];
-                const uint32_t word4[4] = {q.code.x, q.code.y, q.code.z, q.code.w};
-                const __half2 sc = __half2half2(q.scale);
-                if constexpr (C::INT4) {
-                    const __half2 z = __half2half2(q.zero), k1024 = as_h2(0x64006400u);
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t v[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            // 1024 + c, c, c - z, (c - z) s
-                            const __half2 h = as_h2(((word4[j] >> (4 * n)) & 0x000F000Fu) | 0x64006400u);
-                            v[n] = h2(__hmul2(__hsub2(__hsub2(h, k1024), z), sc));
-                        }
-                        out[j] = make_uint4(v[0], v[1], v[2], v[3]);
+                    for (int n = 0; n < 4; ++n) {
+                        // 1024 + c, c, c - z, (c - z) s
+                        const __half2 h = as_h2(((word4[j] >> (4 * n)) & 0x000F000Fu) | 0x64006400u);
+                        v[n] = h2(__hmul2(__hsub2(__hsub2(h, k1024), z), sc));
                     }
-                    const float zf = __half2float(q.zero);
-                    if (fmaxf(fabsf(zf), fabsf(15.f - zf)) * __half2float(q.scale) > 65504.f) {  // may saturate
-                        uint32_t* o = reinterpret_cast<uint32_t*>(out);
-#pragma unroll
-                        for (int n = 0; n < 16; ++n)
-                            o[n] = h2(__hmax2(__hmin2(as_h2(o[n]), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            v[n] = h2(__hmul2(e4m3x2(word4[2 * j + n / 2] >> (16 * (n & 1))), sc));
-                        }
-                        out[j] = make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                    if (__half2float(q.scale) > 65504.f / 448.f) {  // may saturate; NaN codes stay
-                        uint32_t* o = reinterpret_cast<uint32_t*>(out);
-#pragma unroll
-                        for (int n = 0; n < 8; ++n)
-                            o[n] = h2(__hmax2_nan(__hmin2_nan(as_h2(o[n]), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
-                    }
+                    out[j] = make_uint4(v[0], v[1], v[2], v[3]);
                 }
-                if (special) {
-                    const T* src = nullptr;
-                    if (t < s.ctx) {
-                        if (t >= s.w0)
-                            src = static_cast<const T*>(kv ? a.win[1] : a.win[0]) +
-                                  (((static_cast<int64_t>(s.b) * a.ring + (t / BS) % a.ring) * a.hkv + s.kvh) * BS + t % BS) * D;
-                        else if (t < s.sinks)
-                            src = static_cast<const T*>(kv ? a.sink[1] : a.sink[0]) +
-                                  ((static_cast<int64_t>(s.b) * a.n_sink + t) * a.hkv + s.kvh) * D;
-                    }
-                    if (src || t >= s.ctx || cur[x] < 0) {
-#pragma unroll
-                        for (int j = 0; j < C::OUT; ++j)
-                            out[j] = src ? as_fp16<T, PERM>(*reinterpret_cast<const uint4*>(src + (C::OUT * c + j) * 8))
-                                         : make_uint4(0, 0, 0, 0);
-                    }
-                }
-                if (guard) {  // non-finite values: out, and back in for the rows that see them
+                const float zf = __half2float(q.zero);
+                if (fmaxf(fabsf(zf), fabsf(15.f - zf)) * __half2float(q.scale) > 65504.f) {  // may saturate
                     uint32_t* o = reinterpret_cast<uint32_t*>(out);
 #pragma unroll
-                    for (int n = 0; n < 4 * C::OUT; ++n) {
-                        if ((o[n] & 0x7C00u) == 0x7C00u) { o[n] &= 0xffff0000u; odd = true; }
-                        if ((o[n] & 0x7C000000u) == 0x7C000000u) { o[n] &= 0x0000ffffu; odd = true; }
-                    }
+                    for (int n = 0; n < 16; ++n)
+                        o[n] = h2(__hmax2(__hmin2(as_h2(o[n]), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
                 }
-                const int rr = (2 * u + x) * BS + row;
+            } else {
 #pragma unroll
-                for (int j = 0; j < C::OUT; ++j) *reinterpret_cast<uint4*>(tile + tile_off(rr, C::OUT * c + j)) = out[j];
-                load(x, i, kv ^ 1, row0);
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        v[n] = h2(__hmul2(e4m3x2(word4[2 * j + n / 2] >> (16 * (n & 1))), sc));
+                    }
+                    out[j] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                if (__half2float(q.scale) > 65504.f / 448.f) {  // may saturate; NaN codes stay
+                    uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+                        o[n] = h2(__hmax2_nan(__hmin2_nan(as_h2(o[n]), as_h2(0x7BFF7BFFu)), as_h2(0xFBFFFBFFu)));
+                }
             }
+            if (special) {
+                const T* src = nullptr;
+                if (t < s.ctx) {
+                    if (t >= s.w0)
+                        src = static_cast<const T*>(kv ? a.win[1] : a.win[0]) +
+                              (((static_cast<int64_t>(s.b) * a.ring + (t / BS) % a.ring) * a.hkv + s.kvh) * BS + t % BS) * D;
+                    else if (t < s.sinks)
+                        src = static_cast<const T*>(kv ? a.sink[1] : a.sink[0]) +
+                              ((static_cast<int64_t>(s.b) * a.n_sink + t) * a.hkv + s.kvh) * D;
+                }
+                if (src || t >= s.ctx || cur < 0) {
+#pragma unroll
+                    for (int j = 0; j < C::OUT; ++j)
+                        out[j] = src ? as_fp16<T, PERM>(*reinterpret_cast<const uint4*>(src + (C::OUT * c + j) * 8))
+                                     : make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (guard) {  // non-finite values: out, and back in for the rows that see them
+                uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+                for (int n = 0; n < 4 * C::OUT; ++n) {
+                    if ((o[n] & 0x7C00u) == 0x7C00u) { o[n] &= 0xffff0000u; odd = true; }
+                    if ((o[n] & 0x7C000000u) == 0x7C000000u) { o[n] &= 0x0000ffffu; odd = true; }
+                }
+            }
+            const int rr = row_in + row;
+#pragma unroll
+            for (int j = 0; j < C::OUT; ++j) *reinterpret_cast<uint4*>(tile + tile_off(rr, C::OUT * c + j)) = out[j];
+            load(i, kv_next, next);
         }
         if (__any_sync(0xffffffffu, odd) && lane == 0) *sm.odd() = 1;
         fence_async_shared();
@@ -354,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = warp >> 2;  // 0, 1: softmax
     const T* qbase = static_cast<const T*>(a.q) + (static_cast<int64_t>(q0) * a.hq + s.kvh * a.G) * D;
     if (warp == kWarpUnpack && lane == 0) {
-        sm.init(4);
+        sm.init(kBlocks);
     } else if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sh_addr(sm.tmem_slot())),
                      "r"(kTmemCols)
@@ -390,12 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after_sync();
     const uint32_t tmem = *sm.tmem_slot();
 
-    if (tile == 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        unpack_warp<T, D, QMODE, NG>(sm, a, w, s, warp - kWarpUnpack);
-    } else if (tile == 3) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (tile >= 2) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == kWarpMma) mma_warp<__half>(sm, tmem, w, a.status);
+        else unpack_warp<T, D, QMODE, NG>(sm, a, w, s, warp - kWarpUnpack);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         float m, l;
