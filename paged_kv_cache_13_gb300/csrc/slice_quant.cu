@@ -31,9 +31,9 @@ constexpr int BS = 16;
 constexpr int kThreads = 512;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8-14: unpacking; 15: MMAs
 constexpr int kWarpUnpack = 8, kUnpackWarps = 7, kWarpMma = 15;
 constexpr int kBlocks = kKeys / BS;  // blocks of a ring item
-// Registers: launched at 128 a thread, then softmax 176, the others 80.
+// Registers: launched at 128 a thread, then softmax 184, the others 72.
 constexpr int kLaunchRegs = 128;
-static_assert(2 * 128 * 176 + 2 * 128 * 80 <= kThreads * kLaunchRegs, "register split");
+static_assert(2 * 128 * 184 + 2 * 128 * 72 <= kThreads * kLaunchRegs, "register split");
 
 template <int D, int QMODE, int NG>
 struct Codes {
@@ -365,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *sm.tmem_slot();
 
     if (tile >= 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kWarpMma) mma_warp<__half>(sm, tmem, w, a.status);
         else unpack_warp<T, D, QMODE, NG>(sm, a, w, s, warp - kWarpUnpack);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         float m, l;
         const bool ok = softmax_tile<__half>(sm, tmem, w, tile, a.scale_log2, a.status, m, l, [](int) { return true; });
         const int row = w.row0 + tile * kRows + (warp & 3) * 32 + lane;
