@@ -43,26 +43,37 @@ constexpr int kKeys = 128;     // keys per tile
 constexpr int kFirst = 64;     // keys of P handed to the MMAs before the rest is computed
 constexpr int kTmemCols = 512;  // S0, S1, O0, O1: 128 columns each
 
-template <int D>
+// QUEUE: the CTA takes one job after another (see prompt.cu); else one.
+template <int D, bool QUEUE>
 struct Layout {
     static constexpr int kTile = kRows * D * 2;  // bytes of a 128 x D 16-bit tile
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = D == 128 ? (QUEUE ? 4 : 5) : 8;
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = 2 * kTile;
-    static constexpr int kOffBar = kOffRing + kStages * kTile;
+    // output rows on their way out, 64 columns at a time, 16 KiB a row tile: in
+    // Q's place when no other job's Q can be there yet
+    static constexpr int kOffOut = QUEUE ? kOffRing + kStages * kTile : kOffQ;
+    static constexpr int kOutTile = QUEUE ? kRows * 128 : kTile;
+    static constexpr int kOffBar = kOffRing + kStages * kTile + (QUEUE ? 2 * kOutTile : 0);
     // mbarriers: ring slot filled / read, S done (per tile), P written (first
-    // keys of tile 0, 1, then the rest), O done, everything issued done
+    // keys of tile 0, 1, then the rest), O done, everything issued done; with a
+    // queue also Q written, O read (per tile), job written / done with (two),
+    // claim answered
     static constexpr int kFull = 0, kFree = kStages, kS = 2 * kStages, kP = kS + 2, kO = kP + 4, kDrain = kO + 2;
-    static constexpr int kBars = kDrain + 1;
-    static constexpr int kOffVars = kOffBar + 8 * kBars;
-    static constexpr int kBytes = kOffVars + 16;
+    static constexpr int kQ = kDrain + 1, kORead = kQ + 2, kJob = kORead + 2, kJobDone = kJob + 2, kClaim = kJobDone + 2;
+    static constexpr int kBars = QUEUE ? kClaim + 1 : kQ;
+    static constexpr int kOffVars = (kOffBar + 8 * kBars + 15) / 16 * 16;
+    static constexpr int kOffClaim = kOffVars + 16, kOffJobs = kOffClaim + 16, kJobBytes = 80;
+    static constexpr int kBytes = QUEUE ? kOffJobs + 2 * kJobBytes : kOffClaim;
 };
-static_assert(Layout<128>::kBytes <= 232448 && Layout<64>::kBytes <= 232448, "shared memory");
+static_assert(Layout<128, true>::kBytes <= 232448 && Layout<64, true>::kBytes <= 232448 &&
+                  Layout<128, false>::kBytes <= 232448 && Layout<64, false>::kBytes <= 232448,
+              "shared memory");
 
 // A CTA's shared memory.
-template <int D>
+template <int D, bool QUEUE>
 struct Smem {
-    using Y = Layout<D>;
+    using Y = Layout<D, QUEUE>;
     uint8_t* p;
     uint32_t base;
     __device__ __forceinline__ explicit Smem(uint8_t* raw) : p(raw), base(sh_addr(raw)) {}  // raw: 1 KiB-aligned
@@ -70,26 +81,51 @@ struct Smem {
     __device__ __forceinline__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(p + Y::kOffVars); }
     // raised when a wait ran out
     __device__ __forceinline__ volatile int* stop() const { return reinterpret_cast<int*>(p + Y::kOffVars + 4); }
-    // raised when a non-finite V value was taken out of a masked tile
-    __device__ __forceinline__ volatile int* odd() const { return reinterpret_cast<int*>(p + Y::kOffVars + 8); }
+    // raised when a non-finite V value was taken out of a masked tile of job n
+    __device__ __forceinline__ volatile int* odd(int n) const { return reinterpret_cast<int*>(p + Y::kOffVars + 8) + (n & 1); }
     __device__ __forceinline__ bool stopped() const { return *stop() != 0; }
     __device__ __forceinline__ void give_up(int* status) const {
         atomicOr(status, PKV_STATUS_COPY_TIMEOUT);
         *stop() = 1;
     }
-    // ring item 2 jj is K of the jj-th tile, 2 jj + 1 its V
+    // the CTA's ring items in order: of a job, item 2 jj is K of its jj-th
+    // tile, 2 jj + 1 V
     static __device__ __forceinline__ int slot(int it) { return it % Y::kStages; }
     static __device__ __forceinline__ uint32_t phase(int it) { return static_cast<uint32_t>(it / Y::kStages) & 1u; }
     __device__ __forceinline__ uint8_t* ring(int it) const { return p + Y::kOffRing + slot(it) * Y::kTile; }
     // by one thread, before any other uses the barriers; full: arrivals that
-    // fill a ring slot
-    __device__ __forceinline__ void init(int full) const {
-        for (int i = 0; i < Y::kBars; ++i)
-            mbar_init(bar(i), i < Y::kFree ? full : (i >= Y::kP && i < Y::kO ? 4 : 1));
+    // fill a ring slot; readers: warps that read a job
+    __device__ __forceinline__ void init(int full, int readers) const {
+        for (int i = 0; i < Y::kBars; ++i) {
+            int n = 1;
+            if (i < Y::kFree) n = full;
+            if ((i >= Y::kP && i < Y::kO) || (i >= Y::kQ && i < Y::kJob)) n = 4;  // a tile's warps
+            if (i >= Y::kJobDone && i < Y::kClaim) n = readers;
+            mbar_init(bar(i), n);
+        }
         *stop() = 0;
-        *odd() = 0;
+        *odd(0) = 0;
+        *odd(1) = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_shared();
+    }
+};
+
+// What a CTA has done before the job at hand: ring items, key tiles per row
+// tile, jobs in which the row tile had any.  The barriers' phases follow from
+// it.
+struct Before {
+    int items = 0, tiles[2] = {0, 0}, jobs[2] = {0, 0};
+    __device__ __forceinline__ int t(int tile) const { return tile ? tiles[1] : tiles[0]; }
+    __device__ __forceinline__ int j(int tile) const { return tile ? jobs[1] : jobs[0]; }
+    template <typename W>
+    __device__ __forceinline__ void add(const W& w) {
+        items += 2 * w.n;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            tiles[i] += w.cnt[i];
+            jobs[i] += w.cnt[i] > 0;
+        }
     }
 };
 
@@ -133,10 +169,11 @@ __device__ __forceinline__ uint32_t tile_off(int r, int ch) {
 // warp-uniform (base descriptors plus constants) and an MMA of K 16 costs its
 // 64 cycles; issued from a lane of a divergent branch it cost ~110 (8,192
 // tokens: 490 instead of 380 us).
-template <typename T, int D>
-__device__ __forceinline__ void mma_warp(const Smem<D>& sm, uint32_t tmem, const Work& w, int* status) {
-    using Y = Layout<D>;
-    if (w.n == 0) return;
+// One job; false when a wait ran out.
+template <typename T, int D, bool QUEUE>
+__device__ __forceinline__ bool mma_job(const Smem<D, QUEUE>& sm, uint32_t tmem, const Work& w, const Before& before) {
+    using Y = Layout<D, QUEUE>;
+    if (w.n == 0) return true;
     constexpr uint32_t id_s = instr_desc<T>(kKeys, false), id_o = instr_desc<T>(D, true);
     constexpr uint32_t kTile16 = Y::kTile >> 4, kHalf16 = (kRows * 128) >> 4;  // descriptor units
     const bool el = elect();
@@ -161,22 +198,25 @@ __device__ __forceinline__ void mma_warp(const Smem<D>& sm, uint32_t tmem, const
                 mma_ts(tmem + 2 * kKeys + i * kKeys, tmem + i * kKeys + kk * 8, vb + kk * 128, id_o, acc || kk > 0);
         }
     };
-    int s = 0;  // ring slot and its phase, walking K0 V0 K1 V1 ..
-    uint32_t ph = 0;
+    // ring slot and its phase, walking K0 V0 K1 V1 .. (by a shuffle, so that the
+    // compiler takes the slot as warp-uniform)
+    int s = QUEUE ? __shfl_sync(0xffffffffu, sm.slot(before.items), 0) : 0;
+    uint32_t ph = sm.phase(before.items);
     auto next = [&]() {
         if (++s == Y::kStages) {
             s = 0;
             ph ^= 1u;
         }
     };
-    bool ok = wait_bar(sm.bar(Y::kFull), 0);
-    if (ok) {
-        fence_after_sync();
+    bool ok = wait_bar(sm.bar(Y::kFull + s), ph);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (w.cnt[i] > 0) issue_s(i, 0);
-        if (el) mma_commit(sm.bar(Y::kFree));
+    for (int i = 0; i < 2; ++i) {
+        if (!ok || w.cnt[i] == 0) continue;
+        if (QUEUE) ok = wait_bar(sm.bar(Y::kQ + i), before.jobs[i] & 1);
+        fence_after_sync();
+        if (ok) issue_s(i, s);
     }
+    if (ok && el) mma_commit(sm.bar(Y::kFree + s));
     next();
     for (int jj = 0; ok && jj < w.n; ++jj) {
         const int sv = s;  // V(jj), then K(jj + 1)
@@ -186,11 +226,14 @@ __device__ __forceinline__ void mma_warp(const Smem<D>& sm, uint32_t tmem, const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (!ok || jj >= w.cnt[i]) continue;
-            ok = wait_bar(sm.bar(Y::kP + i), jj & 1);
+            const uint32_t turn = (before.tiles[i] + jj) & 1;
+            ok = wait_bar(sm.bar(Y::kP + i), turn);
+            // the last job's O has been read
+            if (QUEUE && ok && jj == 0 && before.jobs[i] > 0) ok = wait_bar(sm.bar(Y::kORead + i), (before.jobs[i] - 1) & 1);
             if (!ok) continue;
             fence_after_sync();
             issue_o(i, sv, 0, kFirst / 16, jj > 0);
-            ok = wait_bar(sm.bar(Y::kP + 2 + i), jj & 1);
+            ok = wait_bar(sm.bar(Y::kP + 2 + i), turn);
             if (!ok) continue;
             fence_after_sync();
             issue_o(i, sv, kFirst / 16, kKeys / 16, true);
@@ -212,21 +255,27 @@ __device__ __forceinline__ void mma_warp(const Smem<D>& sm, uint32_t tmem, const
         }
         next();
     }
-    if (!ok && (threadIdx.x & 31) == 0) sm.give_up(status);
-    // every MMA and every arrival of theirs is done (bounded) before the CTA
-    // gives up its shared memory and TMEM
-    if (el) mma_commit(sm.bar(Y::kDrain));
-    wait_bar(sm.bar(Y::kDrain), 0);
+    return ok;
 }
 
-// The softmax of row tile `tile` by its warpgroup, through all its key tiles
-// and the last O += P V; false when a wait ran out.  m, l: the row's
+// Every MMA and every arrival of theirs is done (bounded) before the CTA gives
+// up its shared memory and TMEM.
+template <int D, bool QUEUE>
+__device__ __forceinline__ void mma_end(const Smem<D, QUEUE>& sm, bool ok, int* status) {
+    if (!ok && (threadIdx.x & 31) == 0) sm.give_up(status);
+    if (elect()) mma_commit(sm.bar(Layout<D, QUEUE>::kDrain));
+    wait_bar(sm.bar(Layout<D, QUEUE>::kDrain), 0);
+}
+
+// The softmax of row tile `tile` by its warpgroup, through all its key tiles;
+// false when a wait ran out.  m, l: the row's
 // reference maximum (base 2) and sum.  before_p(jj): called by the whole warp
 // before tile jj's P is handed over; false to stop.
-template <typename T, int D, typename BeforeP>
-__device__ __forceinline__ bool softmax_tile(const Smem<D>& sm, uint32_t tmem, const Work& w, int tile, float scale_log2,
-                                             int* status, float& m, float& l, BeforeP before_p) {
-    using Y = Layout<D>;
+template <typename T, int D, bool QUEUE, typename BeforeP>
+__device__ __forceinline__ bool softmax_tile(const Smem<D, QUEUE>& sm, uint32_t tmem, const Work& w, const Before& before,
+                                             int tile, float scale_log2, float& m, float& l, BeforeP before_p) {
+    using Y = Layout<D, QUEUE>;
+    const int turn = before.t(tile);
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tS = tmem + tile * kKeys + lanes, tO = tmem + 2 * kKeys + tile * kKeys + lanes;
@@ -243,7 +292,7 @@ __device__ __forceinline__ bool softmax_tile(const Smem<D>& sm, uint32_t tmem, c
     bool ok = true;
     for (int jj = 0; jj < count; ++jj) {
         const int key0 = (w.js + jj) * kKeys;
-        ok = !sm.stopped() && wait_bar(sm.bar(Y::kS + tile), jj & 1);
+        ok = !sm.stopped() && wait_bar(sm.bar(Y::kS + tile), (turn + jj) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -285,14 +334,13 @@ __device__ __forceinline__ bool softmax_tile(const Smem<D>& sm, uint32_t tmem, c
             l *= alpha;
         }
         if (jj > 0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll 1
+            for (int cc = 0; cc < D / 16; ++cc) {  // the scores' registers leave room for 16 columns
+                float o[16];
+                tmem_ld16_wait(tO + cc * 16, o);
 #pragma unroll
-            for (int cc = 0; cc < D / 32; ++cc) {
-                float o[32];
-                tmem_ld32(tO + cc * 32, o);
-                tmem_wait_ld32(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                tmem_st32(tO + cc * 32, reinterpret_cast<const uint32_t*>(o));
+                for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                tmem_st16(tO + cc * 16, reinterpret_cast<const uint32_t*>(o));
             }
         }
         if (!before_p(jj)) {
@@ -323,12 +371,19 @@ __device__ __forceinline__ bool softmax_tile(const Smem<D>& sm, uint32_t tmem, c
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
-    if (ok && count > 0) {
-        ok = wait_bar(sm.bar(Y::kO + tile), 0);
+    return ok;
+}
+
+// The last O += P V of the job is done; ok: of softmax_tile.
+template <int D, bool QUEUE>
+__device__ __forceinline__ bool wait_o(const Smem<D, QUEUE>& sm, const Work& w, const Before& before, int tile, bool ok,
+                                       int* status) {
+    if (ok && w.count(tile) > 0) {
+        ok = wait_bar(sm.bar(Layout<D, QUEUE>::kO + tile), before.j(tile) & 1);
         fence_after_sync();
     }
     ok = __all_sync(0xffffffffu, ok);
-    if (!ok && lane == 0) sm.give_up(status);
+    if (!ok && (threadIdx.x & 31) == 0) sm.give_up(status);
     return ok;
 }
 
@@ -340,55 +395,64 @@ __host__ __device__ constexpr int stored(int e) {
 }
 
 // Writes the warp's 32 rows of O / l of row tile `tile` to out[token * hq +
-// head], through the tile's Q (no longer read) so that they go out in whole
-// 128-byte lines.  fix(d0, o): called before the division with the thread's
-// columns d0 .. d0 + 31 (stored order).
-template <typename TO, int D, bool PERM, typename Fix>
-__device__ __forceinline__ void store_tile(const Smem<D>& sm, uint32_t tmem, const Work& w, int tile, float l, bool ok,
-                                           TO* out, int hq, Fix fix) {
-    using Y = Layout<D>;
-    constexpr int kCh = D / 8, kStep = 32 / kCh;  // 16-byte chunks of a row, rows per store
+// head], 64 columns at a time through shared memory so that they go out in
+// whole 128-byte lines.  fix(d0, o): called before the division with the
+// thread's columns d0 .. d0 + 31 (stored order); read(): once O has been read.
+template <typename TO, int D, bool PERM, bool QUEUE, typename Fix, typename Read>
+__device__ __forceinline__ void store_tile(const Smem<D, QUEUE>& sm, uint32_t tmem, const Work& w, int tile, float l, bool ok,
+                                           TO* out, int hq, Fix fix, Read read) {
+    using Y = Layout<D, QUEUE>;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const uint32_t tO = tmem + 2 * kKeys + tile * kKeys + (static_cast<uint32_t>(warp * 32) << 16);
-    uint8_t* st = sm.p + Y::kOffQ + tile * Y::kTile + warp * 32 * (D * 2);
+    uint8_t* st = sm.p + Y::kOffOut + tile * Y::kOutTile + warp * 32 * 128;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
 #pragma unroll 1
-    for (int cc = 0; cc < D / 32; ++cc) {
-        float o[32];
-        if (w.count(tile) > 0) {
-            tmem_ld32(tO + cc * 32, o);
-            tmem_wait_ld32(o);
-        }
-        fix(cc * 32, o);
-        if (l == 0.f) {
+    for (int half = 0; half < D / 64; ++half) {
+#pragma unroll 1
+        for (int cc = 0; cc < 2; ++cc) {
+            float o[32];
+            // (set either way: a register that only one way sets would be live
+            // all through a loop over jobs)
+            if (w.count(tile) > 0) {
+                tmem_ld32(tO + half * 64 + cc * 32, o);
+                tmem_wait_ld32(o);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+            fix(half * 64 + cc * 32, o);
+            if (l == 0.f) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint4 v;
-            v.x = Half16<TO>::pack(o[8 * c + stored<PERM>(0)] * inv, o[8 * c + stored<PERM>(1)] * inv);
-            v.y = Half16<TO>::pack(o[8 * c + stored<PERM>(2)] * inv, o[8 * c + stored<PERM>(3)] * inv);
-            v.z = Half16<TO>::pack(o[8 * c + stored<PERM>(4)] * inv, o[8 * c + stored<PERM>(5)] * inv);
-            v.w = Half16<TO>::pack(o[8 * c + stored<PERM>(6)] * inv, o[8 * c + stored<PERM>(7)] * inv);
-            *reinterpret_cast<uint4*>(st + lane * (D * 2) + (((cc * 4 + c) ^ (lane & 7)) << 4)) = v;
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint4 v;
+                v.x = Half16<TO>::pack(o[8 * c + stored<PERM>(0)] * inv, o[8 * c + stored<PERM>(1)] * inv);
+                v.y = Half16<TO>::pack(o[8 * c + stored<PERM>(2)] * inv, o[8 * c + stored<PERM>(3)] * inv);
+                v.z = Half16<TO>::pack(o[8 * c + stored<PERM>(4)] * inv, o[8 * c + stored<PERM>(5)] * inv);
+                v.w = Half16<TO>::pack(o[8 * c + stored<PERM>(6)] * inv, o[8 * c + stored<PERM>(7)] * inv);
+                *reinterpret_cast<uint4*>(st + lane * 128 + (((cc * 4 + c) ^ (lane & 7)) << 4)) = v;
+            }
         }
-    }
-    __syncwarp();
-    const int ch = lane % kCh;
-    int rr = lane / kCh, row = w.row0 + tile * kRows + warp * 32 + rr;
-    int t = row / w.G, h = row - t * w.G;
+        if (half + 1 == D / 64) read();
+        __syncwarp();
+        int rr = lane / 8, row = w.row0 + tile * kRows + warp * 32 + rr;
+        int t = row / w.G, h = row - t * w.G;
 #pragma unroll 4
-    for (int x = 0; x < kCh; ++x) {
-        const uint4 v = *reinterpret_cast<const uint4*>(st + rr * (D * 2) + ((ch ^ (rr & 7)) << 4));
-        if (ok && row < w.rows) *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(t) * hq + h) * D + ch * 8) = v;
-        rr += kStep;
-        row += kStep;
-        h += kStep;
-        while (h >= w.G) {
-            h -= w.G;
-            ++t;
+        for (int x = 0; x < 8; ++x) {
+            const uint4 v = *reinterpret_cast<const uint4*>(st + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            if (ok && row < w.rows)
+                *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(t) * hq + h) * D + half * 64 + (lane & 7) * 8) = v;
+            rr += 4;
+            row += 4;
+            h += 4;
+            while (h >= w.G) {
+                h -= w.G;
+                ++t;
+            }
         }
+        __syncwarp();
     }
 }
 

@@ -34,6 +34,10 @@ constexpr int kWarpLoad = 8, kWarpMma = 9;
 // live scores), the third gives its own back down to 88.
 constexpr int kLaunchRegs = 168;
 static_assert(2 * 128 * 208 + 128 * 88 <= kThreads * kLaunchRegs, "register split exceeds the launch's registers");
+// Ring items of a job still to be loaded when the next job is asked for: later,
+// and the answer is waited for; earlier, and a CTA holds a job that another
+// could have begun.
+constexpr int kAhead = 8;
 
 struct PromptArgs {
     const void* q;
@@ -129,67 +133,83 @@ __device__ __forceinline__ void probe(typename Pair<T>::type (&acc)[4], uint4 w)
     for (int i = 0; i < 4; ++i) acc[i] = __hfma2(*reinterpret_cast<const P*>(&x[i]), z, acc[i]);
 }
 
+// A job as the loading warp hands it to the others.
+struct QueuedJob {
+    int some;  // 0: no job is left
+    int kvh, split;
+    Job job;
+    Work w;
+};
+static_assert(sizeof(QueuedJob) <= Layout<64, true>::kJobBytes, "queue entry");
+
+// Asks for a CTA of the grid that has not started, to do its work in its
+// place; the answer (16 bytes) lands at dst.  Not to be called again once it
+// was no.
+__device__ __forceinline__ void claim_cta(uint32_t dst, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+// The claimed CTA's blockIdx.x, or -1.
+__device__ __forceinline__ int claimed_cta(uint32_t src) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.u32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(x)
+        : "r"(src)
+        : "memory");
+    return x;
+}
+
+// One CTA per (slot, KV head, split) is launched; those that fit run, and take
+// over the work of the rest one by one.  What a CTA costs besides its tiles --
+// its start, TMEM, the first Q, K and V, the last output rows: 6 to 9 us -- is
+// then paid once, and between jobs the next one's K and V are already in the
+// ring and its Q in registers when the last product of the one before is done.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ PromptArgs a) {
-    using Y = Layout<D>;
+    using Y = Layout<D, true>;
     constexpr int kCh = D / 8;  // 16-byte chunks per row
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const Smem<D> sm(smem_raw);
+    const Smem<D, true> sm(smem_raw);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    // slots from the last one down: a sequence's later rows see more keys
-    const int per_slot = a.hkv * a.splits;
-    const int u = (gridDim.x - 1 - blockIdx.x) / per_slot;
-    const int kvh = (gridDim.x - 1 - blockIdx.x) % per_slot / a.splits;
-    const int split = (gridDim.x - 1 - blockIdx.x) % a.splits;
-
-    if (blockIdx.x == 0 && warp == kWarpMma) {  // the ranges are checked once per call
-        bool bad = false;
-        for (int j = lane; j < a.batch; j += 32) {
-            const int q0 = a.q_start[j], q1 = a.q_start[j + 1], k0 = a.kv_start[j], k1 = a.kv_start[j + 1];
-            bad |= q0 < 0 || q1 < q0 || q1 > a.T || k0 < 0 || k1 < k0 || k1 > a.S || k1 - k0 < q1 - q0;
-        }
-        if (bad) atomicOr(a.status, PKV_STATUS_BAD_CONTEXT);
-    }
-    Job job;
-    if (!find_job(a.q_start, a.kv_start, a.batch, a.T, a.S, a.G, u, job)) return;
-    Work w;
-    w.row0 = job.row0;
-    w.rows = job.rows;
-    w.G = a.G;
-    w.first_pos = job.first_pos;
-    w.set_tiles(split, a.splits);
-
-    auto load_item = [&](int it) {
-        const uint32_t full = sm.bar(Y::kFull + sm.slot(it));
-        mbar_arrive_expect_tx(full, Y::kTile);
-        tma_load(sm.base + Y::kOffRing + sm.slot(it) * Y::kTile, it & 1 ? &vmap : &kmap,
-                 job.k0 + (w.js + it / 2) * kKeys, kvh, full);
+    const int tile = warp >> 2;  // softmax: 0 or 1
+    // CTA x's job: slots from the last one down, a sequence's later rows see
+    // more keys
+    auto find = [&](int x, QueuedJob& j) {
+        const int y = gridDim.x - 1 - x, per_slot = a.hkv * a.splits;
+        j.kvh = y % per_slot / a.splits;
+        j.split = y % a.splits;
+        return find_job(a.q_start, a.kv_start, a.batch, a.T, a.S, a.G, y / per_slot, j.job);
     };
-    const int early = min(2 * w.n, Y::kStages);  // items the empty ring takes
-    const int tile = warp >> 2;                  // softmax: 0 or 1
-    if (warp == kWarpLoad && lane == 0) {
-        sm.init(1);
-        for (int it = 0; it < early; ++it) load_item(it);  // on their way while Q is fetched
-    } else if (warp == kWarpMma) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sh_addr(sm.tmem_slot())),
-                     "r"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    } else if (tile < 2) {
-        // the warp's 32 query rows, whole 128-byte lines at a time: lane l
-        // takes chunk l % kCh of rows l / kCh, l / kCh + kStep, ..
-        constexpr int kStep = 32 / kCh, kLoads = 32 / kStep;
-        const int rr0 = (warp & 3) * 32 + lane / kCh, ch = lane % kCh;
-        int row = w.row0 + tile * kRows + rr0;
+    auto entry = [&](int n) { return reinterpret_cast<QueuedJob*>(sm.p + Y::kOffJobs + (n & 1) * Y::kJobBytes); };
+    // job n (whole warp); false when there is none, or the wait ran out
+    auto next_job = [&](int n) {
+        const bool ok = __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kJob + (n & 1)), (n >> 1) & 1));
+        if (!ok && lane == 0) sm.give_up(a.status);
+        return ok && entry(n)->some != 0;
+    };
+    auto done_with = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.bar(Y::kJobDone + (n & 1)));
+    };
+    // a softmax warp's 32 query rows, whole 128-byte lines at a time: lane l
+    // takes chunk l % kCh of rows l / kCh, l / kCh + kStep, ..
+    constexpr int kStep = 32 / kCh, kLoads = 32 / kStep;
+    auto load_q = [&](const Job& job, int kvh, uint4 (&v)[kLoads]) {
+        int row = job.row0 + tile * kRows + (warp & 3) * 32 + lane / kCh;
         int tok = row / a.G, h = row - tok * a.G;
-        const T* base = static_cast<const T*>(a.q) + static_cast<int64_t>(job.q0) * a.qs + kvh * a.G * D + ch * 8;
-        uint4 v[kLoads];
+        const T* base = static_cast<const T*>(a.q) + static_cast<int64_t>(job.q0) * a.qs + kvh * a.G * D + lane % kCh * 8;
 #pragma unroll
         for (int x = 0; x < kLoads; ++x) {
             v[x] = make_uint4(0, 0, 0, 0);
-            if (row < w.rows) v[x] = *reinterpret_cast<const uint4*>(base + tok * a.qs + h * D);
+            if (row < job.rows) v[x] = *reinterpret_cast<const uint4*>(base + tok * a.qs + h * D);
             row += kStep;
             h += kStep;
             while (h >= a.G) {
@@ -197,10 +217,111 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++tok;
             }
         }
+    };
+    auto put_q = [&](const uint4 (&v)[kLoads]) {
 #pragma unroll
         for (int x = 0; x < kLoads; ++x)
-            *reinterpret_cast<uint4*>(sm.p + Y::kOffQ + tile * Y::kTile + tile_off(rr0 + x * kStep, ch)) = v[x];
+            *reinterpret_cast<uint4*>(sm.p + Y::kOffQ + tile * Y::kTile +
+                                      tile_off((warp & 3) * 32 + lane / kCh + x * kStep, lane % kCh)) = v[x];
         fence_async_shared();
+    };
+    auto q_written = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.bar(Y::kQ + tile));
+    };
+
+    // ---- the loading warp: jobs and their K and V
+    int cta = blockIdx.x;  // the CTA whose job is next; -1: none
+    QueuedJob job = {};
+    Before before;
+    int n = 0;  // jobs handed out
+    bool asked = false, unchecked = cta == 0;
+    uint32_t asked_phase = 0;
+    auto load_item = [&](int i) {  // of the job
+        const int it = before.items + i;
+        const uint32_t full = sm.bar(Y::kFull + sm.slot(it));
+        mbar_arrive_expect_tx(full, Y::kTile);
+        tma_load(sm.base + Y::kOffRing + sm.slot(it) * Y::kTile, i & 1 ? &vmap : &kmap,
+                 job.job.k0 + (job.w.js + i / 2) * kKeys, job.kvh, full);
+    };
+    auto ask = [&]() {
+        if (asked) return;
+        asked = true;
+        if (lane == 0) {
+            fence_async_shared();  // the last answer has been read
+            mbar_arrive_expect_tx(sm.bar(Y::kClaim), 16);
+            claim_cta(sm.base + Y::kOffClaim, sm.bar(Y::kClaim));
+        }
+        __syncwarp();
+    };
+    auto answer = [&]() {  // false when it did not come
+        if (!__all_sync(0xffffffffu, wait_bar(sm.bar(Y::kClaim), asked_phase))) return false;
+        asked = false;
+        asked_phase ^= 1u;
+        cta = claimed_cta(sm.base + Y::kOffClaim);
+        unchecked |= cta == 0;
+        __syncwarp();
+        return true;
+    };
+    auto check = [&]() {  // the ranges, once per call
+        if (!unchecked) return;
+        unchecked = false;
+        bool bad = false;
+        for (int j = lane; j < a.batch; j += 32) {
+            const int q0 = a.q_start[j], q1 = a.q_start[j + 1], k0 = a.kv_start[j], k1 = a.kv_start[j + 1];
+            bad |= q0 < 0 || q1 < q0 || q1 > a.T || k0 < 0 || k1 < k0 || k1 > a.S || k1 - k0 < q1 - q0;
+        }
+        if (bad) atomicOr(a.status, PKV_STATUS_BAD_CONTEXT);
+    };
+    // job n for the others; false when a wait ran out
+    auto hand_out = [&]() {
+        bool ok = true;
+        while (cta >= 0 && !find(cta, job)) {
+            ask();
+            ok = answer();
+            if (!ok) return false;
+        }
+        if (n >= 2) ok = __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kJobDone + (n & 1)), ((n >> 1) - 1) & 1));
+        if (!ok) return false;
+        job.some = cta >= 0;
+        if (cta >= 0) {
+            job.w.row0 = job.job.row0;
+            job.w.rows = job.job.rows;
+            job.w.G = a.G;
+            job.w.first_pos = job.job.first_pos;
+            job.w.set_tiles(job.split, a.splits);
+        }
+        if (lane == 0) {
+            *entry(n) = job;
+            *sm.odd(n) = 0;
+            mbar_arrive(sm.bar(Y::kJob + (n & 1)));
+        }
+        __syncwarp();
+        return true;
+    };
+
+    bool first = false;  // softmax: the CTA's own job has rows of the tile's, its Q is in place
+    int early = 0;
+    if (warp == kWarpLoad) {
+        if (lane == 0) sm.init(1, 9);
+        __syncwarp();
+        if (hand_out() && cta >= 0) {
+            early = min(2 * job.w.n, Y::kStages);  // items the empty ring takes, on their way while Q is fetched
+            if (lane == 0)
+                for (int i = 0; i < early; ++i) load_item(i);
+        }
+    } else if (warp == kWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sh_addr(sm.tmem_slot())),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (tile < 2) {
+        first = find(blockIdx.x, job);
+        if (first) {
+            uint4 v[kLoads];
+            load_q(job.job, job.kvh, v);
+            put_q(v);
+        }
     }
     fence_before_sync();
     __syncthreads();
@@ -209,85 +330,151 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tile == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == kWarpLoad && lane == 0) {
-            int it = early;
-            for (; it < 2 * w.n && !sm.stopped(); ++it) {
-                if (!wait_bar(sm.bar(Y::kFree + sm.slot(it)), sm.phase(it - Y::kStages))) {
-                    sm.give_up(a.status);
-                    break;
+        if (warp == kWarpLoad) {
+            bool ok = true;
+            while (ok && cta >= 0) {
+                int i = early;
+                early = 0;
+                for (; i < 2 * job.w.n && ok; ++i) {
+                    if (i + kAhead >= 2 * job.w.n) ask();  // the next job
+                    const int it = before.items + i;
+                    if (it >= Y::kStages)
+                        ok = !__any_sync(0xffffffffu, sm.stopped()) &&
+                             __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFree + sm.slot(it)), sm.phase(it - Y::kStages)));
+                    if (ok && lane == 0) load_item(i);
+                    __syncwarp();
                 }
-                load_item(it);
+                before.add(job.w);
+                if (!ok) before.items += i - 1 - 2 * job.w.n;  // those issued
+                check();
+                if (!ok) break;
+                ask();
+                ok = answer();
+                if (ok) {
+                    ++n;
+                    ok = hand_out();
+                }
             }
-            // stopping early: the copies in flight land (bounded) before the
-            // shared memory is given up
-            if (sm.stopped())
-                for (int x = max(it - Y::kStages, 0); x < it; ++x) wait_bar(sm.bar(Y::kFull + sm.slot(x)), sm.phase(x));
+            check();
+            if (!ok && lane == 0) sm.give_up(a.status);
+            // stopping early: the copies and the answer in flight land
+            // (bounded) before the shared memory is given up
+            if (!ok) {
+                for (int x = max(before.items - Y::kStages, 0); x < before.items; ++x)
+                    wait_bar(sm.bar(Y::kFull + sm.slot(x)), sm.phase(x));
+                if (asked) wait_bar(sm.bar(Y::kClaim), asked_phase);
+            }
         } else if (warp == kWarpMma) {
-            mma_warp<T>(sm, tmem, w, a.status);
+            bool ok = true;
+            for (; ok && next_job(n); ++n) {
+                const Work w = entry(n)->w;
+                done_with(n);
+                ok = mma_job<T>(sm, tmem, w, before);
+                before.add(w);
+            }
+            mma_end(sm, ok, a.status);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        // a tile with keys that some row must not see: its V rows may hold
-        // anything there; tile 0 looks, tile 1 once tile 0 is done
-        auto scan = [&](int jj) {
-            if (!w.masked(jj) || (tile == 1 && jj < w.cnt[0])) return true;
-            const int it = 2 * jj + 1;
-            if (!__all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFull + sm.slot(it)), sm.phase(it)))) return false;
-            uint8_t* vt = sm.ring(it) + (warp & 3) * 32 * 128;  // the warp's 32 rows
-            typename Pair<T>::type acc[4];
-            const uint32_t zero = 0;
+        bool some = next_job(0);
+        if (some && entry(0)->w.count(tile) > 0) {
+            if (!first) {
+                uint4 v[kLoads];
+                load_q(entry(0)->job, entry(0)->kvh, v);
+                put_q(v);
+            }
+            q_written();
+        }
+        while (some) {
+            const Work w = entry(n)->w;
+            // a tile with keys that some row must not see: its V rows may hold
+            // anything there; tile 0 looks, tile 1 once tile 0 is done
+            auto scan = [&](int jj) {
+                if (!w.masked(jj) || (tile == 1 && jj < w.cnt[0])) return true;
+                const int it = before.items + 2 * jj + 1;
+                if (!__all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFull + sm.slot(it)), sm.phase(it)))) return false;
+                uint8_t* vt = sm.ring(it) + (warp & 3) * 32 * 128;  // the warp's 32 rows
+                typename Pair<T>::type acc[4];
+                const uint32_t zero = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = *reinterpret_cast<const typename Pair<T>::type*>(&zero);
-            auto chunk = [&](int c) {
-                return reinterpret_cast<uint4*>(vt + (c / 8) * (kRows * 128) + (c % 8) * 512 + lane * 16);
-            };
+                for (int i = 0; i < 4; ++i) acc[i] = *reinterpret_cast<const typename Pair<T>::type*>(&zero);
+                auto chunk = [&](int c) {
+                    return reinterpret_cast<uint4*>(vt + (c / 8) * (kRows * 128) + (c % 8) * 512 + lane * 16);
+                };
 #pragma unroll 4
-            for (int c = 0; c < kCh; ++c) probe<T>(acc, *chunk(c));
-            bool odd = false;
+                for (int c = 0; c < kCh; ++c) probe<T>(acc, *chunk(c));
+                bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = make_float2(Half16<T>::to_float(acc[i].x), Half16<T>::to_float(acc[i].y));
-                odd |= f.x != f.x || f.y != f.y;
-            }
-            if (__any_sync(0xffffffffu, odd)) {
-                if (lane == 0) *sm.odd() = 1;
-                constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = make_float2(Half16<T>::to_float(acc[i].x), Half16<T>::to_float(acc[i].y));
+                    odd |= f.x != f.x || f.y != f.y;
+                }
+                if (__any_sync(0xffffffffu, odd)) {
+                    if (lane == 0) *sm.odd(n) = 1;
+                    constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
 #pragma unroll 1
-                for (int c = 0; c < kCh; ++c) {
-                    uint16_t* e = reinterpret_cast<uint16_t*>(chunk(c));
-                    for (int i = 0; i < 8; ++i)
-                        if ((e[i] & kExp) == kExp) e[i] = 0;
+                    for (int c = 0; c < kCh; ++c) {
+                        uint16_t* e = reinterpret_cast<uint16_t*>(chunk(c));
+                        for (int i = 0; i < 8; ++i)
+                            if ((e[i] & kExp) == kExp) e[i] = 0;
+                    }
+                    fence_async_shared();
                 }
-                fence_async_shared();
-            }
-            return true;
-        };
-        float m, l;
-        const bool ok = softmax_tile<T>(sm, tmem, w, tile, a.scale_log2, a.status, m, l, scan);
-        // non-finite V values that were taken out come back for the rows that
-        // see them (their weight is positive)
-        const int row = w.row0 + tile * kRows + (warp & 3) * 32 + lane;
-        const bool odd = w.count(tile) > 0 && *sm.odd() != 0;
-        const int my_pos = w.first_pos + min(row, w.rows - 1) / a.G;
-        auto put_back = [&](int d0, float (&o)[32]) {
-            if (!odd) return;
-            for (int t = w.masked_from(); t <= my_pos && t < min((w.js + w.n) * kKeys, job.S); ++t) {
-                const T* vr = static_cast<const T*>(a.v) + (static_cast<int64_t>(job.k0) + t) * a.vs + kvh * D + d0;
+                return true;
+            };
+            float m, l;
+            bool ok = softmax_tile<T>(sm, tmem, w, before, tile, a.scale_log2, m, l, scan);
+            // the next job's Q: fetched while the last product is computed,
+            // written when that has read this one's
+            const bool more = ok && next_job(n + 1);
+            const bool has_q = more && entry(n + 1)->w.count(tile) > 0;
+            uint4 v[kLoads];  // set either way: else live all through the loop
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float f = Half16<T>::to_float(vr[i]);
-                    if (!(fabsf(f) <= 3.4e38f)) o[i] += f;
-                }
+            for (int i = 0; i < kLoads; ++i) v[i] = make_uint4(0, 0, 0, 0);
+            if (has_q) load_q(entry(n + 1)->job, entry(n + 1)->kvh, v);
+            ok = wait_o(sm, w, before, tile, ok, a.status);
+            if (has_q) {
+                put_q(v);
+                q_written();
             }
-        };
-        const int64_t head0 = static_cast<int64_t>(job.q0) * a.hq + kvh * a.G;  // row (token 0, head 0) of the output
-        if (a.splits == 1) {
-            store_tile<T, D, false>(sm, tmem, w, tile, l, ok, static_cast<T*>(a.out) + head0 * D, a.hq, put_back);
-        } else {
-            const int tok = row / a.G;
-            const int64_t prow = static_cast<int64_t>(split) * a.T * a.hq + head0 + static_cast<int64_t>(tok) * a.hq +
-                                 (row - tok * a.G);
-            store_partial<D, false>(tmem, w, tile, m, l, ok && row < w.rows, a.ws_o, a.ws_ml, prow, put_back);
+            const QueuedJob job = *entry(n);
+            // non-finite V values that were taken out come back for the rows
+            // that see them (their weight is positive)
+            const int row = w.row0 + tile * kRows + (warp & 3) * 32 + lane;
+            const bool odd = w.count(tile) > 0 && *sm.odd(n) != 0;
+            const int my_pos = w.first_pos + min(row, w.rows - 1) / a.G;
+            auto put_back = [&](int d0, float (&o)[32]) {
+                if (!odd) return;
+                for (int t = w.masked_from(); t <= my_pos && t < min((w.js + w.n) * kKeys, job.job.S); ++t) {
+                    const T* vr = static_cast<const T*>(a.v) + (static_cast<int64_t>(job.job.k0) + t) * a.vs + job.kvh * D + d0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float f = Half16<T>::to_float(vr[i]);
+                        if (!(fabsf(f) <= 3.4e38f)) o[i] += f;
+                    }
+                }
+            };
+            auto o_read = [&]() {
+                if (w.count(tile) == 0) return;
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sm.bar(Y::kORead + tile));
+            };
+            const int64_t head0 = static_cast<int64_t>(job.job.q0) * a.hq + job.kvh * a.G;  // row (token 0, head 0) of the output
+            if (a.splits == 1) {
+                store_tile<T, D, false>(sm, tmem, w, tile, l, ok, static_cast<T*>(a.out) + head0 * D, a.hq, put_back, o_read);
+            } else {
+                const int tok = row / a.G;
+                const int64_t prow = static_cast<int64_t>(job.split) * a.T * a.hq + head0 +
+                                     static_cast<int64_t>(tok) * a.hq + (row - tok * a.G);
+                store_partial<D, false>(tmem, w, tile, m, l, ok && row < w.rows, a.ws_o, a.ws_ml, prow, put_back);
+                o_read();
+            }
+            done_with(n);
+            if (!ok) break;
+            before.add(w);
+            some = more;
+            ++n;
         }
     }
     fence_before_sync();
@@ -363,11 +550,11 @@ int prompt_splits(int64_t batch, int64_t T, int64_t S, int64_t hkv, int64_t G) {
 
 template <typename T, int D>
 int launch_prompt(const CUtensorMap& km, const CUtensorMap& vm, const PromptArgs& a, cudaStream_t st) {
-    const int rc = prepare_kernel<prompt_tc_kernel<T, D>>(Layout<D>::kBytes, kLaunchRegs);
+    const int rc = prepare_kernel<prompt_tc_kernel<T, D>>(Layout<D, true>::kBytes, kLaunchRegs);
     if (rc != PKV_OK) return rc;
     const int64_t slots = num_slots(a.batch, a.T, a.G);
     const unsigned ctas = static_cast<unsigned>(slots * a.hkv);
-    prompt_tc_kernel<T, D><<<ctas * a.splits, kThreads, Layout<D>::kBytes, st>>>(km, vm, a);
+    prompt_tc_kernel<T, D><<<ctas * a.splits, kThreads, Layout<D, true>::kBytes, st>>>(km, vm, a);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
     if (a.splits == 1) return PKV_OK;
     cudaLaunchConfig_t cfg = {};

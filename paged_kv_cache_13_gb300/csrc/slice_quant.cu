@@ -31,9 +31,9 @@ constexpr int BS = 16;
 constexpr int kThreads = 512;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8-14: unpacking; 15: MMAs
 constexpr int kWarpUnpack = 8, kUnpackWarps = 7, kWarpMma = 15;
 constexpr int kBlocks = kKeys / BS;  // blocks of a ring item
-// Registers: launched at 128 a thread, then softmax 184, the others 72.
+// Registers: launched at 128 a thread, then softmax 176, the others 80.
 constexpr int kLaunchRegs = 128;
-static_assert(2 * 128 * 184 + 2 * 128 * 72 <= kThreads * kLaunchRegs, "register split");
+static_assert(2 * 128 * 176 + 2 * 128 * 80 <= kThreads * kLaunchRegs, "register split");
 
 template <int D, int QMODE, int NG>
 struct Codes {
@@ -114,9 +114,9 @@ __device__ float value_at(const QuantCache& a, const Seq& s, int t, int d) {
 // before is unpacked and its table entry a job earlier still (the codes'
 // addresses wait for it).
 template <typename T, int D, int QMODE, int NG>
-__device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache& a, const Work& w, const Seq& s, int u) {
+__device__ __forceinline__ void unpack_warp(const Smem<D, false>& sm, const QuantCache& a, const Work& w, const Seq& s, int u) {
     using C = Codes<D, QMODE, NG>;
-    using Y = Layout<D>;
+    using Y = Layout<D, false>;
     constexpr bool PERM = C::INT4;
     const int lane = threadIdx.x & 31, r = lane % C::RPI, c = lane / C::RPI;
     const int gi = NG == 2 ? c / (C::CPR / 2) : 0;
@@ -287,7 +287,7 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
             for (int j = 0; j < C::OUT; ++j) *reinterpret_cast<uint4*>(tile + tile_off(rr, C::OUT * c + j)) = out[j];
             load(i, kv_next, next);
         }
-        if (__any_sync(0xffffffffu, odd) && lane == 0) *sm.odd() = 1;
+        if (__any_sync(0xffffffffu, odd) && lane == 0) *sm.odd(0) = 1;
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(sm.bar(Y::kFull + sm.slot(it)));
@@ -298,11 +298,11 @@ __device__ __forceinline__ void unpack_warp(const Smem<D>& sm, const QuantCache&
 template <typename T, int D, int QMODE, int NG>
 __global__ void __launch_bounds__(kThreads, 1)
     slice_tc_kernel(const __grid_constant__ QuantCache a, int splits, float* ws_o, float* ws_ml) {
-    using Y = Layout<D>;
+    using Y = Layout<D, false>;
     constexpr bool PERM = QMODE == PKV_QMODE_INT4_ASYM;
     constexpr int kCh = D / 8;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const Smem<D> sm(smem_raw);
+    const Smem<D, false> sm(smem_raw);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     // a sequence's later rows see more keys: they go first
     const int x = gridDim.x - 1 - blockIdx.x, split = x % splits, tile_row = x / splits;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = warp >> 2;  // 0, 1: softmax
     const T* qbase = static_cast<const T*>(a.q) + (static_cast<int64_t>(q0) * a.hq + s.kvh * a.G) * D;
     if (warp == kWarpUnpack && lane == 0) {
-        sm.init(kBlocks);
+        sm.init(kBlocks, 0);
     } else if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sh_addr(sm.tmem_slot())),
                      "r"(kTmemCols)
@@ -365,16 +365,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *sm.tmem_slot();
 
     if (tile >= 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == kWarpMma) mma_warp<__half>(sm, tmem, w, a.status);
-        else unpack_warp<T, D, QMODE, NG>(sm, a, w, s, warp - kWarpUnpack);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == kWarpMma) {
+            mma_end(sm, mma_job<__half>(sm, tmem, w, Before()), a.status);
+        } else {
+            unpack_warp<T, D, QMODE, NG>(sm, a, w, s, warp - kWarpUnpack);
+        }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         float m, l;
-        const bool ok = softmax_tile<__half>(sm, tmem, w, tile, a.scale_log2, a.status, m, l, [](int) { return true; });
+        bool ok = softmax_tile<__half>(sm, tmem, w, Before(), tile, a.scale_log2, m, l, [](int) { return true; });
+        ok = wait_o(sm, w, Before(), tile, ok, a.status);
         const int row = w.row0 + tile * kRows + (warp & 3) * 32 + lane;
         const int tok = row / a.G, h = row - tok * a.G;
-        const bool odd = w.count(tile) > 0 && *sm.odd() != 0;
+        const bool odd = w.count(tile) > 0 && *sm.odd(0) != 0;
         const int my_pos = w.first_pos + min(row, w.rows - 1) / a.G;
         auto put_back = [&](int d0, float (&o)[32]) {
             if (!odd) return;
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (splits == 1) {
             store_tile<T, D, PERM>(sm, tmem, w, tile, l, ok,
                                    static_cast<T*>(a.out) + (static_cast<int64_t>(q0) * a.hq + s.kvh * a.G) * D, a.hq,
-                                   put_back);
+                                   put_back, [] {});
         } else {
             const int64_t prow = ((static_cast<int64_t>(split) * a.batch + s.b) * a.max_q_len + tok) * a.hq + s.kvh * a.G + h;
             store_partial<D, PERM>(tmem, w, tile, m, l, ok && row < w.rows, ws_o, ws_ml, prow, put_back);
@@ -430,13 +434,13 @@ int slice_splits(int64_t batch, int64_t hkv, int64_t G, int64_t max_blocks, int6
 
 template <typename T, int D, int QMODE, int NG>
 int launch(const QuantCache& a, float* workspace, cudaStream_t st) {
-    const int rc = prepare_kernel<slice_tc_kernel<T, D, QMODE, NG>>(Layout<D>::kBytes, kLaunchRegs);
+    const int rc = prepare_kernel<slice_tc_kernel<T, D, QMODE, NG>>(Layout<D, false>::kBytes, kLaunchRegs);
     if (rc != PKV_OK) return rc;
     const int splits = slice_splits(a.batch, a.hkv, a.G, a.max_blocks, a.max_q_len);
     const unsigned tiles = static_cast<unsigned>(row_tiles(a.max_q_len, a.G));
     float* ws_ml = splits > 1 ? workspace + static_cast<size_t>(splits) * a.batch * a.max_q_len * a.hq * D : nullptr;
     slice_tc_kernel<T, D, QMODE, NG>
-        <<<dim3(tiles * splits, a.hkv, a.batch), kThreads, Layout<D>::kBytes, st>>>(a, splits, workspace, ws_ml);
+        <<<dim3(tiles * splits, a.hkv, a.batch), kThreads, Layout<D, false>::kBytes, st>>>(a, splits, workspace, ws_ml);
     if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
     if (splits == 1) return PKV_OK;
     cudaLaunchConfig_t cfg = {};
