@@ -48,6 +48,7 @@ template <int D, bool QUEUE>
 struct Layout {
     static constexpr int kTile = kRows * D * 2;  // bytes of a 128 x D 16-bit tile
     static constexpr int kStages = D == 128 ? (QUEUE ? 4 : 5) : 8;
+    static constexpr int kQueue = 4;  // jobs handed out and not done with, at most
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = 2 * kTile;
     // output rows on their way out, 64 columns at a time, 16 KiB a row tile: in
@@ -57,14 +58,15 @@ struct Layout {
     static constexpr int kOffBar = kOffRing + kStages * kTile + (QUEUE ? 2 * kOutTile : 0);
     // mbarriers: ring slot filled / read, S done (per tile), P written (first
     // keys of tile 0, 1, then the rest), O done, everything issued done; with a
-    // queue also Q written, O read (per tile), job written / done with (two),
-    // claim answered
+    // queue also Q written, O read (per tile), job written / done with (per
+    // entry), claim answered
     static constexpr int kFull = 0, kFree = kStages, kS = 2 * kStages, kP = kS + 2, kO = kP + 4, kDrain = kO + 2;
-    static constexpr int kQ = kDrain + 1, kORead = kQ + 2, kJob = kORead + 2, kJobDone = kJob + 2, kClaim = kJobDone + 2;
+    static constexpr int kQ = kDrain + 1, kORead = kQ + 2, kJob = kORead + 2, kJobDone = kJob + kQueue,
+                         kClaim = kJobDone + kQueue;
     static constexpr int kBars = QUEUE ? kClaim + 1 : kQ;
     static constexpr int kOffVars = (kOffBar + 8 * kBars + 15) / 16 * 16;
-    static constexpr int kOffClaim = kOffVars + 16, kOffJobs = kOffClaim + 16, kJobBytes = 80;
-    static constexpr int kBytes = QUEUE ? kOffJobs + 2 * kJobBytes : kOffClaim;
+    static constexpr int kOffClaim = kOffVars + 32, kOffJobs = kOffClaim + 16, kJobBytes = 80;
+    static constexpr int kBytes = QUEUE ? kOffJobs + kQueue * kJobBytes : kOffClaim;
 };
 static_assert(Layout<128, true>::kBytes <= 232448 && Layout<64, true>::kBytes <= 232448 &&
                   Layout<128, false>::kBytes <= 232448 && Layout<64, false>::kBytes <= 232448,
@@ -82,7 +84,7 @@ struct Smem {
     // raised when a wait ran out
     __device__ __forceinline__ volatile int* stop() const { return reinterpret_cast<int*>(p + Y::kOffVars + 4); }
     // raised when a non-finite V value was taken out of a masked tile of job n
-    __device__ __forceinline__ volatile int* odd(int n) const { return reinterpret_cast<int*>(p + Y::kOffVars + 8) + (n & 1); }
+    __device__ __forceinline__ volatile int* odd(int n) const { return reinterpret_cast<int*>(p + Y::kOffVars + 8) + n % Y::kQueue; }
     __device__ __forceinline__ bool stopped() const { return *stop() != 0; }
     __device__ __forceinline__ void give_up(int* status) const {
         atomicOr(status, PKV_STATUS_COPY_TIMEOUT);
@@ -104,8 +106,7 @@ struct Smem {
             mbar_init(bar(i), n);
         }
         *stop() = 0;
-        *odd(0) = 0;
-        *odd(1) = 0;
+        for (int i = 0; i < Y::kQueue; ++i) *odd(i) = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_shared();
     }

@@ -35,8 +35,8 @@ constexpr int kWarpLoad = 8, kWarpMma = 9;
 constexpr int kLaunchRegs = 168;
 static_assert(2 * 128 * 208 + 128 * 88 <= kThreads * kLaunchRegs, "register split exceeds the launch's registers");
 // Ring items of a job still to be loaded when the next job is asked for: later,
-// and the answer is waited for; earlier, and a CTA holds a job that another
-// could have begun.
+// and the ring runs empty; earlier, and a CTA holds a job that another could
+// have begun.
 constexpr int kAhead = 8;
 
 struct PromptArgs {
@@ -53,58 +53,68 @@ struct PromptArgs {
     int* status;
 };
 
-// The rows of one CTA.  Slot u of the grid belongs to the last sequence b
-// with off(b) = floor(q_start[b] G / 256) + b <= u and is its rows 256 (u -
-// off(b)) ..: off(b + 1) - off(b) is at least the sequence's 256-row tiles,
-// so each has a slot, and the grid's size follows from T and the batch alone.
+// The rows of one CTA.  The grid has num_slots = floor(T G / 256) + batch slots
+// of 256 rows, counted from the last down: a sequence's later rows see more
+// keys.  Up to 31 sequences each has exactly its tiles' slots, and those left
+// over come last; of more, sequence b's start at off(b) = floor(q_start[b] G /
+// 256) + b: off(b + 1) - off(b) is at least its tiles.
 struct Job {
     int b, q0, L, k0, S, first_pos;
     int row0, rows;  // first row in the sequence, rows of the sequence (see Work)
 };
 
-// Warp-collective; false when the slot has no rows.
+// The y-th slot from the last.  Warp-collective; false when it has no rows.
 __device__ __forceinline__ bool find_job(const int32_t* q_start, const int32_t* kv_start, int batch, int T, int S, int G,
-                                         int u, Job& job) {
+                                         int y, Job& job) {
     const int lane = threadIdx.x & 31;
     auto start = [&](int b) { return min(max(q_start[b], 0), T); };
-    int lo = 0, n = batch;
+    int lo = 0;
     int qa, qe, ka, ke;
+    int64_t row0;
     if (batch < 32) {  // every start in one round of loads
         const int qv = lane <= batch ? start(lane) : 0, kv = lane <= batch ? min(max(kv_start[lane], 0), S) : 0;
-        const unsigned le = __ballot_sync(0xffffffffu, lane < batch &&
-                                                           static_cast<int64_t>(qv) * G / kCtaRows + lane <= u);
-        if (le == 0) return false;
-        lo = __popc(le) - 1;
+        const int qn = __shfl_down_sync(0xffffffffu, qv, 1);
+        const int tiles = lane < batch && qn > qv
+                              ? static_cast<int>((static_cast<int64_t>(qn - qv) * G + kCtaRows - 1) / kCtaRows)
+                              : 0;
+        int sum = tiles;  // of sequences 0 .. lane
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += x;
+        }
+        const int u = __shfl_sync(0xffffffffu, sum, 31) - 1 - y;
+        if (u < 0) return false;
+        lo = __popc(__ballot_sync(0xffffffffu, sum <= u));
         qa = __shfl_sync(0xffffffffu, qv, lo);
         qe = __shfl_sync(0xffffffffu, qv, lo + 1);
         ka = __shfl_sync(0xffffffffu, kv, lo);
         ke = __shfl_sync(0xffffffffu, kv, lo + 1);
+        row0 = static_cast<int64_t>(u - __shfl_sync(0xffffffffu, sum - tiles, lo)) * kCtaRows;
     } else {
-    for (;;) {
-        const int step = (n + 31) / 32;
-        const int b = lo + lane * step;
-        const bool le = lane * step < n &&
-                        static_cast<int64_t>(start(b)) * G / kCtaRows + b <= u;
-        const int c = __popc(__ballot_sync(0xffffffffu, le));
-        if (c == 0) return false;
-        lo += (c - 1) * step;
-        n = min(step, n - (c - 1) * step);
-        if (n == 1) break;
-    }
-    qa = start(lo);
-    qe = start(lo + 1);
-    ka = min(max(kv_start[lo], 0), S);
-    ke = min(max(kv_start[lo + 1], 0), S);
+        const int64_t u = static_cast<int64_t>(T) * G / kCtaRows + batch - 1 - y;
+        for (int n = batch;;) {
+            const int step = (n + 31) / 32;
+            const int b = lo + lane * step;
+            const bool le = lane * step < n && static_cast<int64_t>(start(b)) * G / kCtaRows + b <= u;
+            const int c = __popc(__ballot_sync(0xffffffffu, le));
+            if (c == 0) return false;
+            lo += (c - 1) * step;
+            n = min(step, n - (c - 1) * step);
+            if (n == 1) break;
+        }
+        qa = start(lo);
+        qe = start(lo + 1);
+        ka = min(max(kv_start[lo], 0), S);
+        ke = min(max(kv_start[lo + 1], 0), S);
+        row0 = (u - (static_cast<int64_t>(qa) * G / kCtaRows + lo)) * kCtaRows;
     }
     job.b = lo;
     job.q0 = qa;
     job.L = qe - qa;
     job.k0 = ka;
     job.S = max(ke - ka, 0);
-    if (job.L <= 0) return false;
-    const int64_t off = static_cast<int64_t>(job.q0) * G / kCtaRows + lo;
-    const int64_t row0 = (u - off) * kCtaRows;
-    if (row0 < 0 || row0 >= static_cast<int64_t>(job.L) * G) return false;  // < 0: starts out of order
+    if (job.L <= 0 || row0 < 0 || row0 >= static_cast<int64_t>(job.L) * G) return false;  // < 0: starts out of order
     job.row0 = static_cast<int>(row0);
     job.rows = job.L * G;
     job.first_pos = job.S - job.L;
@@ -180,24 +190,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Smem<D, true> sm(smem_raw);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int tile = warp >> 2;  // softmax: 0 or 1
-    // CTA x's job: slots from the last one down, a sequence's later rows see
-    // more keys
-    auto find = [&](int x, QueuedJob& j) {
-        const int y = gridDim.x - 1 - x, per_slot = a.hkv * a.splits;
-        j.kvh = y % per_slot / a.splits;
-        j.split = y % a.splits;
-        return find_job(a.q_start, a.kv_start, a.batch, a.T, a.S, a.G, y / per_slot, j.job);
+    auto find = [&](int x, QueuedJob& j) {  // CTA x's job
+        const int per_slot = a.hkv * a.splits;
+        j.kvh = x % per_slot / a.splits;
+        j.split = x % a.splits;
+        return find_job(a.q_start, a.kv_start, a.batch, a.T, a.S, a.G, x / per_slot, j.job);
     };
-    auto entry = [&](int n) { return reinterpret_cast<QueuedJob*>(sm.p + Y::kOffJobs + (n & 1) * Y::kJobBytes); };
+    auto entry = [&](int n) { return reinterpret_cast<QueuedJob*>(sm.p + Y::kOffJobs + n % Y::kQueue * Y::kJobBytes); };
     // job n (whole warp); false when there is none, or the wait ran out
     auto next_job = [&](int n) {
-        const bool ok = __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kJob + (n & 1)), (n >> 1) & 1));
+        const bool ok = __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kJob + n % Y::kQueue), n / Y::kQueue & 1));
         if (!ok && lane == 0) sm.give_up(a.status);
         return ok && entry(n)->some != 0;
     };
     auto done_with = [&](int n) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm.bar(Y::kJobDone + (n & 1)));
+        if (lane == 0) mbar_arrive(sm.bar(Y::kJobDone + n % Y::kQueue));
     };
     // a softmax warp's 32 query rows, whole 128-byte lines at a time: lane l
     // takes chunk l % kCh of rows l / kCh, l / kCh + kStep, ..
@@ -237,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n = 0;  // jobs handed out
     bool asked = false, unchecked = cta == 0;
     uint32_t asked_phase = 0;
-    auto load_item = [&](int i) {  // of the job
+    auto load_item = [&](const QueuedJob& job, int i) {
         const int it = before.items + i;
         const uint32_t full = sm.bar(Y::kFull + sm.slot(it));
         mbar_arrive_expect_tx(full, Y::kTile);
@@ -273,15 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (bad) atomicOr(a.status, PKV_STATUS_BAD_CONTEXT);
     };
-    // job n for the others; false when a wait ran out
-    auto hand_out = [&]() {
+    // CTA `cta`'s job (or the next that has rows) to the others as job n; false
+    // when a wait ran out
+    auto hand_out = [&](QueuedJob& job) {
         bool ok = true;
         while (cta >= 0 && !find(cta, job)) {
+            if (a.batch < 32) {  // nor has any CTA behind it
+                cta = -1;
+                break;
+            }
             ask();
-            ok = answer();
-            if (!ok) return false;
+            if (!answer()) return false;
         }
-        if (n >= 2) ok = __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kJobDone + (n & 1)), ((n >> 1) - 1) & 1));
+        if (n >= Y::kQueue)
+            ok = __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kJobDone + n % Y::kQueue), (n / Y::kQueue - 1) & 1));
         if (!ok) return false;
         job.some = cta >= 0;
         if (cta >= 0) {
@@ -294,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             *entry(n) = job;
             *sm.odd(n) = 0;
-            mbar_arrive(sm.bar(Y::kJob + (n & 1)));
+            mbar_arrive(sm.bar(Y::kJob + n % Y::kQueue));
         }
         __syncwarp();
         return true;
@@ -305,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpLoad) {
         if (lane == 0) sm.init(1, 9);
         __syncwarp();
-        if (hand_out() && cta >= 0) {
+        if (hand_out(job) && cta >= 0) {
             early = min(2 * job.w.n, Y::kStages);  // items the empty ring takes, on their way while Q is fetched
             if (lane == 0)
-                for (int i = 0; i < early; ++i) load_item(i);
+                for (int i = 0; i < early; ++i) load_item(job, i);
         }
     } else if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sh_addr(sm.tmem_slot())),
@@ -332,28 +345,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == kWarpLoad) {
             bool ok = true;
-            while (ok && cta >= 0) {
+            bool some = cta >= 0;
+            while (ok && some) {
+                // the next job is asked for and handed out in time for its
+                // first items to follow this one's last, behind what the ring
+                // holds
+                const int items = 2 * job.w.n, at = max(min(items, Y::kStages), items - kAhead);
+                QueuedJob after = {};
                 int i = early;
                 early = 0;
-                for (; i < 2 * job.w.n && ok; ++i) {
-                    if (i + kAhead >= 2 * job.w.n) ask();  // the next job
+                some = false;
+                for (;; ++i) {
+                    if (i == at) {
+                        check();
+                        ask();
+                        ok = answer();
+                        if (ok) {
+                            ++n;
+                            ok = hand_out(after);
+                            some = cta >= 0;
+                        }
+                    }
+                    if (!ok || i >= items) break;
                     const int it = before.items + i;
                     if (it >= Y::kStages)
                         ok = !__any_sync(0xffffffffu, sm.stopped()) &&
                              __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFree + sm.slot(it)), sm.phase(it - Y::kStages)));
-                    if (ok && lane == 0) load_item(i);
+                    if (!ok) break;
+                    if (lane == 0) load_item(job, i);
                     __syncwarp();
                 }
-                before.add(job.w);
-                if (!ok) before.items += i - 1 - 2 * job.w.n;  // those issued
-                check();
-                if (!ok) break;
-                ask();
-                ok = answer();
-                if (ok) {
-                    ++n;
-                    ok = hand_out();
-                }
+                before.items += i;
+                job = after;
             }
             check();
             if (!ok && lane == 0) sm.give_up(a.status);
@@ -490,9 +513,9 @@ constexpr int kMergeWarps = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) prompt_merge_kernel(const __grid_constant__ PromptArgs a) {
-    const int u = blockIdx.x / a.hkv, kvh = blockIdx.x % a.hkv;
+    const int kvh = blockIdx.x % a.hkv;
     Job job;
-    const bool any = find_job(a.q_start, a.kv_start, a.batch, a.T, a.S, a.G, u, job);
+    const bool any = find_job(a.q_start, a.kv_start, a.batch, a.T, a.S, a.G, blockIdx.x / a.hkv, job);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!any) return;
     const int end = min(job.row0 + kCtaRows, job.rows);
