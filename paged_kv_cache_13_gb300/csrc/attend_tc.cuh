@@ -59,11 +59,12 @@ struct Layout {
     // mbarriers: ring slot filled / read, S done (per tile), P written (first
     // keys of tile 0, 1, then the rest), O done, everything issued done; with a
     // queue also Q written, O read (per tile), job written / done with (per
-    // entry), claim answered
+    // entry), claim answered, V looked through (per slot; see prompt.cu)
     static constexpr int kFull = 0, kFree = kStages, kS = 2 * kStages, kP = kS + 2, kO = kP + 4, kDrain = kO + 2;
     static constexpr int kQ = kDrain + 1, kORead = kQ + 2, kJob = kORead + 2, kJobDone = kJob + kQueue,
-                         kClaim = kJobDone + kQueue;
-    static constexpr int kBars = QUEUE ? kClaim + 1 : kQ;
+                         kClaim = kJobDone + kQueue, kClean = kClaim + 1;
+    static constexpr int kBars = QUEUE ? kClean + kStages : kQ;
+    static_assert(!QUEUE || kStages % 2 == 0, "V in the odd slots");
     static constexpr int kOffVars = (kOffBar + 8 * kBars + 15) / 16 * 16;
     static constexpr int kOffClaim = kOffVars + 32, kOffJobs = kOffClaim + 16, kJobBytes = 80;
     static constexpr int kBytes = QUEUE ? kOffJobs + kQueue * kJobBytes : kOffClaim;
@@ -102,7 +103,8 @@ struct Smem {
             int n = 1;
             if (i < Y::kFree) n = full;
             if ((i >= Y::kP && i < Y::kO) || (i >= Y::kQ && i < Y::kJob)) n = 4;  // a tile's warps
-            if (i >= Y::kJobDone && i < Y::kClaim) n = readers;
+            if (QUEUE && i >= Y::kJobDone && i < Y::kClaim) n = readers;
+            if (QUEUE && i >= Y::kClean) n = 2;
             mbar_init(bar(i), n);
         }
         *stop() = 0;
@@ -222,6 +224,7 @@ __device__ __forceinline__ bool mma_job(const Smem<D, QUEUE>& sm, uint32_t tmem,
     for (int jj = 0; ok && jj < w.n; ++jj) {
         const int sv = s;  // V(jj), then K(jj + 1)
         ok = !sm.stopped() && wait_bar(sm.bar(Y::kFull + sv), ph);
+        if (QUEUE && ok) ok = wait_bar(sm.bar(Y::kClean + sv), ph);
         next();
         bool have_k = false;
 #pragma unroll
@@ -272,9 +275,9 @@ __device__ __forceinline__ void mma_end(const Smem<D, QUEUE>& sm, bool ok, int* 
 // false when a wait ran out.  m, l: the row's
 // reference maximum (base 2) and sum.  before_p(jj): called by the whole warp
 // before tile jj's P is handed over; false to stop.
-template <typename T, int D, bool QUEUE, typename BeforeP>
+template <typename T, int D, bool QUEUE>
 __device__ __forceinline__ bool softmax_tile(const Smem<D, QUEUE>& sm, uint32_t tmem, const Work& w, const Before& before,
-                                             int tile, float scale_log2, float& m, float& l, BeforeP before_p) {
+                                             int tile, float scale_log2, float& m, float& l) {
     using Y = Layout<D, QUEUE>;
     const int turn = before.t(tile);
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -343,10 +346,6 @@ __device__ __forceinline__ bool softmax_tile(const Smem<D, QUEUE>& sm, uint32_t 
                 for (int i = 0; i < 16; ++i) o[i] *= alpha;
                 tmem_st16(tO + cc * 16, reinterpret_cast<const uint32_t*>(o));
             }
-        }
-        if (!before_p(jj)) {
-            ok = false;
-            break;
         }
         const float mref = m == neg_inf() ? 0.f : m;
         const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-mref, -mref);

@@ -28,7 +28,7 @@ namespace {
 
 using namespace tcattn;
 
-constexpr int kThreads = 384;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8: copies; 9: MMAs
+constexpr int kThreads = 384;  // warps 0-3, 4-7: softmax of tiles 0, 1; 8: copies; 9: MMAs; 10, 11: V's non-finite values
 constexpr int kWarpLoad = 8, kWarpMma = 9;
 // Registers: launched at 168 a thread; the softmax warpgroups take 208 (128
 // live scores), the third gives its own back down to 88.
@@ -141,6 +141,37 @@ __device__ __forceinline__ void probe(typename Pair<T>::type (&acc)[4], uint4 w)
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = __hfma2(*reinterpret_cast<const P*>(&x[i]), z, acc[i]);
+}
+
+// Takes the non-finite values out of 64 rows of a V tile (a warp; any order
+// will do, so the swizzle does not matter); true when there were any.
+template <typename T, int D>
+__device__ __forceinline__ bool clean_rows(uint8_t* p) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kPer = kRows / 2 * 128 / 512;  // 512-byte pieces of a 64-column half
+    auto piece = [&](int c) { return reinterpret_cast<uint4*>(p + c / kPer * (kRows * 128) + c % kPer * 512 + lane * 16); };
+    typename Pair<T>::type acc[4];
+    const uint32_t zero = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = *reinterpret_cast<const typename Pair<T>::type*>(&zero);
+#pragma unroll 8
+    for (int c = 0; c < D / 64 * kPer; ++c) probe<T>(acc, *piece(c));
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = make_float2(Half16<T>::to_float(acc[i].x), Half16<T>::to_float(acc[i].y));
+        odd |= f.x != f.x || f.y != f.y;
+    }
+    if (!__any_sync(0xffffffffu, odd)) return false;
+    constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+#pragma unroll 1
+    for (int c = 0; c < D / 64 * kPer; ++c) {
+        uint16_t* e = reinterpret_cast<uint16_t*>(piece(c));
+        for (int i = 0; i < 8; ++i)
+            if ((e[i] & kExp) == kExp) e[i] = 0;
+    }
+    fence_async_shared();
+    return true;
 }
 
 // A job as the loading warp hands it to the others.
@@ -316,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool first = false;  // softmax: the CTA's own job has rows of the tile's, its Q is in place
     int early = 0;
     if (warp == kWarpLoad) {
-        if (lane == 0) sm.init(1, 9);
+        if (lane == 0) sm.init(1, 11);
         __syncwarp();
         if (hand_out(job) && cta >= 0) {
             early = min(2 * job.w.n, Y::kStages);  // items the empty ring takes, on their way while Q is fetched
@@ -396,6 +427,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 before.add(w);
             }
             mma_end(sm, ok, a.status);
+        } else {
+            // The V tiles of every job before their products.  A tile with keys
+            // that some row must not see may hold anything there (0 x NaN would
+            // reach that row): its non-finite values are taken out.  By warps of
+            // their own, ahead of the products: in the softmax warps it cost 3 us
+            // a job.  Each takes half of the rows.
+            bool ok = true;
+            for (; ok && next_job(n); ++n) {
+                const Work w = entry(n)->w;
+                for (int jj = 0; jj < w.n && ok; ++jj) {
+                    const int it = before.items + 2 * jj + 1;
+                    ok = !__any_sync(0xffffffffu, sm.stopped()) &&
+                         __all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFull + sm.slot(it)), sm.phase(it)));
+                    if (!ok) break;
+                    if (w.masked(jj) && clean_rows<T, D>(sm.ring(it) + (warp & 1) * (kRows / 2) * 128) && lane == 0)
+                        *sm.odd(n) = 1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sm.bar(Y::kClean + sm.slot(it)));
+                }
+                before.items += 2 * w.n;
+                done_with(n);
+            }
+            if (!ok && lane == 0) sm.give_up(a.status);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -410,43 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         while (some) {
             const Work w = entry(n)->w;
-            // a tile with keys that some row must not see: its V rows may hold
-            // anything there; tile 0 looks, tile 1 once tile 0 is done
-            auto scan = [&](int jj) {
-                if (!w.masked(jj) || (tile == 1 && jj < w.cnt[0])) return true;
-                const int it = before.items + 2 * jj + 1;
-                if (!__all_sync(0xffffffffu, wait_bar(sm.bar(Y::kFull + sm.slot(it)), sm.phase(it)))) return false;
-                uint8_t* vt = sm.ring(it) + (warp & 3) * 32 * 128;  // the warp's 32 rows
-                typename Pair<T>::type acc[4];
-                const uint32_t zero = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = *reinterpret_cast<const typename Pair<T>::type*>(&zero);
-                auto chunk = [&](int c) {
-                    return reinterpret_cast<uint4*>(vt + (c / 8) * (kRows * 128) + (c % 8) * 512 + lane * 16);
-                };
-#pragma unroll 4
-                for (int c = 0; c < kCh; ++c) probe<T>(acc, *chunk(c));
-                bool odd = false;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = make_float2(Half16<T>::to_float(acc[i].x), Half16<T>::to_float(acc[i].y));
-                    odd |= f.x != f.x || f.y != f.y;
-                }
-                if (__any_sync(0xffffffffu, odd)) {
-                    if (lane == 0) *sm.odd(n) = 1;
-                    constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
-#pragma unroll 1
-                    for (int c = 0; c < kCh; ++c) {
-                        uint16_t* e = reinterpret_cast<uint16_t*>(chunk(c));
-                        for (int i = 0; i < 8; ++i)
-                            if ((e[i] & kExp) == kExp) e[i] = 0;
-                    }
-                    fence_async_shared();
-                }
-                return true;
-            };
             float m, l;
-            bool ok = softmax_tile<T>(sm, tmem, w, before, tile, a.scale_log2, m, l, scan);
+            bool ok = softmax_tile<T>(sm, tmem, w, before, tile, a.scale_log2, m, l);
             // the next job's Q: fetched while the last product is computed,
             // written when that has read this one's
             const bool more = ok && next_job(n + 1);

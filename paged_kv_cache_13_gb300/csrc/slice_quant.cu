@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         float m, l;
-        bool ok = softmax_tile<__half>(sm, tmem, w, Before(), tile, a.scale_log2, m, l, [](int) { return true; });
+        bool ok = softmax_tile<__half>(sm, tmem, w, Before(), tile, a.scale_log2, m, l);
         ok = wait_o(sm, w, Before(), tile, ok, a.status);
         const int row = w.row0 + tile * kRows + (warp & 3) * 32 + lane;
         const int tok = row / a.G, h = row - tok * a.G;
