@@ -237,6 +237,57 @@ def test_repeats_streams_and_graph_replay_give_the_same_bits(pkv, cuda_dev):
         assert torch.equal(out, y)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,top,hkv,d,dtype", [(40, 200, 8, 128, "bf16"), (31, 330, 8, 64, "fp16"), (70, 90, 4, 128, "fp16"),
+                                                   (32, 130, 8, 64, "bf16")])
+def test_more_rows_than_the_device_takes_at_once(pkv, cuda_dev, batch, top, hkv, d, dtype):
+    # several (sequence, KV head) pairs of 256 rows for each SM, empty sequences
+    # and prefixes among them
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, top, batch)
+    lens[::7] = 0
+    lens[1::7] = 1
+    prefix = rng.integers(0, 150, batch) * (rng.random(batch) < 0.4)
+    kv = (lens + prefix).tolist()
+    lens = lens.tolist()
+    q, k, v, qs, ks = inputs(lens, kv, 4 * hkv, hkv, d, dtype, batch, cuda_dev, lead=3, tail=130)
+    out = run(pkv, q, k, v, qs, ks, 0.11)
+    check(q, k, v, qs, ks, 0.11, out)
+    assert torch.equal(out, run(pkv, q, k, v, qs, ks, 0.11))
+    # a bad value in one sequence reaches its own later rows alone, not what the
+    # same SM computes next
+    b = int(np.argmax(lens))
+    at = int(ks[b + 1]) - lens[b] // 2 - 1
+    row = int(qs[b + 1]) - lens[b] // 2 - 1
+    v2 = v.clone()
+    v2[at, 1, 7] = float("nan")
+    v2[int(ks[-1]):] = float("inf")  # rows of no sequence
+    got = run(pkv, q, k, v2, qs, ks, 0.11)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[row:int(qs[b + 1]), 4:8, 7] = True
+    assert torch.equal(got[~hit], out[~hit]) and torch.isnan(got[hit]).all()
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(pkv, cuda_dev):
+    # both larger than the device: neither waits for the other's rows
+    a = inputs([900] * 6, [900] * 6, 32, 8, 128, "bf16", 21, cuda_dev)
+    b = inputs([70] * 50, [300] * 50, 32, 8, 64, "fp16", 22, cuda_dev)
+    first = [run(pkv, *x, 0.1) for x in (a, b)]
+    starts = [[torch.from_numpy(s).to(cuda_dev) for s in x[3:]] for x in (a, b)]
+    outs = [torch.zeros_like(x[0]) for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        for x, (qs, ks), out, s in zip((a, b), starts, outs, streams):
+            with torch.cuda.stream(s):
+                pkv.pkv_prompt_attention(*x[:3], qs, 0.1, out, kv_start=ks)
+    torch.cuda.synchronize()
+    assert pkv.pkv_device_status() == 0
+    assert all(torch.equal(o, f) for o, f in zip(outs, first))
+
+
 def test_refusals(pkv):
     L = pkv.lib
     ok = dict(q=16, k=16, v=16, qs=16, ks=None, batch=1, T=4, S=4, hq=8, hkv=2, d=128, sq=1024, sk=256, sv=256,
