@@ -25,7 +25,9 @@
 // a long context of codes that are all positive, less the zero points', would
 // lose ten bits to cancellation (16k tokens: 1.5e-3 relative).  FP8 codes
 // convert exactly.  sum_t W_t (z_t - 8) is one more MMA per n-tile: the zero
-// points as a 17th row of V.
+// points as a 17th row of V, for fp16 what rounding z - 8 left as an 18th
+// (without it outputs were off by 4.2e-4 instead of 2.9e-4; bf16 ones, off by
+// 1.8e-3 either way, would pay 6% of the time for it).
 // Sinks and window blocks are 16-bit blocks attended after the quantised ones
 // of a run, with the accumulator taken to true units first.
 //
@@ -45,6 +47,8 @@
 #include "balanced.cuh"
 #include "slice_quant.cuh"
 #include "tc5.cuh"
+
+#include <type_traits>
 
 namespace pkv {
 namespace {
@@ -92,6 +96,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "r"(addr));
     return r;
 }
+template <typename T>
+constexpr bool kFine = std::is_same<T, __half>::value;  // see Scales
 template <typename T>
 constexpr bool kSplitP = false;
 template <>
@@ -203,7 +209,8 @@ struct VCodes {
 
 // K scale / zero of tokens g, g + 8; V scale of the same tokens; V zero points
 // of tokens 2c, 2c + 1 and 8 + 2c, 9 + 2c as fragment words.
-template <int D, int QMODE, int NG>
+// FINE: with what the rounding of z - 8 leaves.
+template <int D, int QMODE, int NG, bool FINE>
 struct Scales {
     __half2 ks[NG], vs[NG], kz[NG];  // low: token g, high: token g + 8
     uint32_t vz[NG][2];
@@ -230,10 +237,17 @@ struct Scales {
                 vz[0][1] = __byte_perm(y.x, y.y, 0x5410u);
                 vz[NG - 1][1] = __byte_perm(y.x, y.y, 0x7632u);
             }
+            // z - 8, as V's codes are taken: lanes g = 0 (row 0 of the zero
+            // points' MMA) hold it rounded, lanes g = 1 what the rounding left
+            // (exact for |z| <= 8; nothing is left from 4 up), the others 0
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {  // z - 8, as V's codes are taken
-                vz[i][0] = sub16x2(vz[i][0], 0x48004800u);
-                vz[i][1] = sub16x2(vz[i][1], 0x48004800u);
+            for (int i = 0; i < NG; ++i) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t hi = sub16x2(vz[i][k], 0x48004800u);
+                    const uint32_t lo = FINE ? sub16x2(vz[i][k], sub16x2(hi, 0xC800C800u)) : 0u;
+                    vz[i][k] = g == 0 ? hi : FINE && g == 1 ? lo : 0u;
+                }
             }
         }
     }
@@ -241,8 +255,8 @@ struct Scales {
 
 // A warp's state over its run: lane (g, c) holds rows 8 nt + 2c (x), 8 nt + 2c +
 // 1 (y) of every n-tile.  nm: minus the reference maximum.  corr: the
-// zero-point MMA's accumulator (rows 0 and 8 of its 16: column groups 0 and 1;
-// lanes g = 0).
+// zero-point MMA's accumulator (rows 0, 1 and 8, 9 of its 16: column groups 0
+// and 1; lanes g = 0, 1).
 template <int MT, int NT>
 struct State {
     float2 nm[NT], l[NT];
@@ -479,7 +493,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             }
             KCodes<D, QMODE, NG> kc;
             kc.load(stage + g * S::CB + (!S::INT4 ? 16 * c : NG == 2 ? 8 * c : (KW == 4 ? 16 * c : 8 * c)));
-            Scales<D, QMODE, NG> sc;
+            Scales<D, QMODE, NG, kFine<T>> sc;
             sc.load(stage + 2 * S::CODES, g, c);
             // ---- S^T = C Q^T over the code values, per column group
             float s[NG][NT][4];
@@ -619,14 +633,14 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
                     b1[gi][nt] = movmatrix_trans(f16pair(w1.x, w1.y));
                 }
             }
-            // ---- sum_t W_t z_t: zero points as row 0 (group 0) and 8 (group 1)
+            // ---- sum_t W_t (z_t - 8): zero points as rows 0, 1 (group 0) and 8, 9
+            // (group 1)
             if constexpr (S::INT4) {
-                const uint32_t on = g == 0 ? 0xffffffffu : 0u;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(w.corr[nt], sc.vz[0][0] & on, 0u, sc.vz[0][1] & on, 0u, b0[0][nt], b1[0][nt]);
+                    mma_f16(w.corr[nt], sc.vz[0][0], 0u, sc.vz[0][1], 0u, b0[0][nt], b1[0][nt]);
                     if constexpr (NG == 2)
-                        mma_f16(w.corr[nt], 0u, sc.vz[NG - 1][0] & on, 0u, sc.vz[NG - 1][1] & on, b0[NG - 1][nt],
+                        mma_f16(w.corr[nt], 0u, sc.vz[NG - 1][0], 0u, sc.vz[NG - 1][1], b0[NG - 1][nt],
                                 b1[NG - 1][nt]);
                 }
             }
@@ -657,7 +671,10 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NT))
             for (int nt = 0; nt < NT; ++nt) {
                 float cr[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) cr[j] = __shfl_sync(0xffffffffu, w.corr[nt][j], c);
+                for (int j = 0; j < 4; ++j) {
+                    cr[j] = __shfl_sync(0xffffffffu, w.corr[nt][j], c);
+                    if constexpr (kFine<T>) cr[j] += __shfl_sync(0xffffffffu, w.corr[nt][j], 4 + c);
+                }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const int el = pv_e<D, NG>(mt, 0);
